@@ -21,8 +21,10 @@
  * wait that runs out sets SD_DEVERR_TIMEOUT and the kernel returns.  No kernel traps.
  *
  * Element types: SD_F32 = IEEE binary32, SD_BF16 = bfloat16 (upper half of a binary32),
- * SD_F16 = IEEE binary16 (only where a call says so: sd_block_pool's output and the
- * indexer's q and k together).  Arithmetic is fp32 (fp64 for the importance score)
+ * SD_F16 = IEEE binary16 (only where a call says so: sd_block_pool's output, the
+ * indexer's q and k together, sd_q8_append's source and sd_verify_drafts' probabilities),
+ * SD_I8 = int8 and SD_E4M3 = 8-bit floats with 4 exponent and 3 mantissa bits (the codes of
+ * an 8-bit cache only).  Arithmetic is fp32 (fp64 for the importance score)
  * whatever the storage type.
  *
  * Sources the operations follow (web pages, cited by title and section):
@@ -54,7 +56,7 @@ typedef enum {
     SD_ERR_TIMEOUT = 5        /* reserved: reported through *err_word, see below */
 } sd_status;
 
-typedef enum { SD_F32 = 0, SD_BF16 = 1, SD_F16 = 2 } sd_dtype;
+typedef enum { SD_F32 = 0, SD_BF16 = 1, SD_F16 = 2, SD_I8 = 3, SD_E4M3 = 4 } sd_dtype;
 
 /* Bits a kernel ORs into *err_word. */
 #define SD_DEVERR_INDEX 0x1   /* a selected index outside [0, N) or [0, T) was skipped */
@@ -514,6 +516,124 @@ sd_status sd_tier_classify(const double* s, int B, int T, const double cum_frac[
 sd_status sd_quantize_rows_int8(const void* x, sd_dtype dtype, const uint8_t* tier, int B,
                                 int Hkv, int T, int d, int8_t* codes, float* scales,
                                 void* stream);
+
+/*
+ * sd_q8_append -- new tokens' K/V rows quantised as they are written into an 8-bit cache.
+ * [HBM] Metodologia 1 (rows kept "e.g. 8-bit"); here every row of the cache is, from the
+ * moment it is written, so no full-precision copy is kept.  For new token i < n of sequence b
+ * with i < count[b] (count NULL: all n), and every KV head h, the cache row t = pos0[b] + i
+ * receives, for x = k_new[b,h,i,:] and likewise for V:
+ *     a = max_j |x_j|;  scale[b,h,t] = a / top;  codes[b,h,t,j] = round(x_j * (top / a))
+ * with top = 127 (SD_I8: round half to even, clamped to +-127) or 448 (SD_E4M3: rounded to the
+ * nearest e4m3 value, ties to even, saturating); every division and product is one correctly
+ * rounded fp32 operation.  A row with a < 2^-100 is stored as scale 0 and zero codes.  Other
+ * rows of the cache are left as they are.  For SD_I8 the same codes and scales as
+ * sd_quantize_rows_int8 gives (down to a = 2^-100).  NaN and infinities are outside the contract.
+ * k_new, v_new: [B,Hkv,n,d] of dtype (F32, BF16 or F16) with the d elements of a row contiguous
+ * and the strides below (in elements, multiples of 16 bytes), e.g. a projection's [B,n,Hkv,d]
+ * output.  codes [B,Hkv,T,d] of code_dtype, scales [B,Hkv,T] fp32.  A row outside [0, T) is
+ * skipped and sets SD_DEVERR_INDEX.  Limits: d in {64, 128}, B*Hkv*n < 2^30.  Launched as a
+ * programmatic dependent of the preceding kernel.
+ */
+typedef struct {
+    const void* k_new;        /* [B,Hkv,n,d] of dtype, strided */
+    const void* v_new;
+    sd_dtype dtype;           /* SD_F32, SD_BF16 or SD_F16 */
+    int B, Hkv, n, d, T;
+    long long k_stride_b, k_stride_h, k_stride_n;  /* elements between sequences, heads, tokens */
+    long long v_stride_b, v_stride_h, v_stride_n;
+    const int32_t* pos0;      /* [B] device: cache row of the first new token */
+    const int32_t* count;     /* nullable [B] device: new tokens of each sequence, at most n */
+    sd_dtype code_dtype;      /* SD_I8 or SD_E4M3 */
+    void* k_codes;            /* [B,Hkv,T,d] */
+    void* v_codes;
+    float* k_scale;           /* [B,Hkv,T] */
+    float* v_scale;
+    int32_t* err_word;        /* nullable device int32 */
+} sd_q8_append_args;
+
+sd_status sd_q8_append(const sd_q8_append_args* args, void* stream);
+
+/*
+ * sd_cache_attend -- exact softmax attention of a serving batch: every sequence over its own
+ * cache (8-bit or bf16, each query token up to its own position) and over a prefix that all
+ * sequences share.
+ * [Illusion] sec. 2 (exact softmax over the attended rows, selected or all); [HBM] Metodologia
+ * 1 (8-bit rows) and 3 (a row contributes the same terms wherever it is stored); [DHiSparse]
+ * "Metodologia" (the query tokens of a verify batch share each fetched row, causal among the
+ * drafts; here the sequences share the prefix's rows as well).
+ * For query row (b, v, h), kvh = h / (Hq/Hkv), the attended rows are
+ *     own rows t (all t < T, or those of idx) with t <= qpos[b,v], with the key
+ *         cache_dtype SD_BF16: k_cache[b,kvh,t,:], else k_scale[b,kvh,t] * k_cache[b,kvh,t,:]
+ *         (V alike), and
+ *     prefix rows j < P with the key k_prefix[kvh,j,:] (every query token sees all of them),
+ *     z = scale * q . key;  out[b,v,h,:] = sum softmax(z) V;  lse[b,v,h] = log sum exp(z).
+ * No rows (qpos[b,v] < 0 and P = 0): out = 0, lse = -inf.  The new tokens' own rows are part
+ * of the cache (append first, then attend with qpos = their positions); a padding query token
+ * has qpos = -1.  qpos entries beyond T - 1 act as T - 1.
+ * idx (nullable, [B,Hkv,n_idx]): the own rows are idx[b,kvh,j / block] * block + j % block, j <
+ * n_idx * block, those beyond qpos[b,v] left out; -1 is an empty slot, other entries outside
+ * the cache are skipped and set SD_DEVERR_INDEX; an entry given twice counts twice.
+ * q [B,V,Hq,d] bf16; k_cache, v_cache [B,Hkv,T,d] of cache_dtype (SD_BF16, SD_I8 or SD_E4M3);
+ * k_scale, v_scale [B,Hkv,T] fp32, finite and >= 0 (8-bit caches only); k_prefix, v_prefix
+ * [Hkv,P,d] bf16 (P = 0: none).  Attended bf16 rows are finite; so are rows up to the largest
+ * qpos of their sequence.  Rows beyond it, and their scales, may hold anything.
+ * out [B,V,Hq,d] of out_dtype: SD_F32 (softmax weights kept to 16 or more significant bits) or
+ * SD_BF16 (weights rounded once to 8 bits, 11 over an 8-bit cache); lse [B,V,Hq] fp32.  Sums
+ * and softmax statistics are fp32.  The split of the work, and so the summation order, depends
+ * on the sizes, qpos and the GPU, not on the data; equal calls give equal bits.
+ * Limits: d in {64, 128}, G*V <= 32 (G = Hq/Hkv), B <= 65535.
+ * The workspace (sd_cache_attend_workspace_bytes, a host computation over the sizes) holds the
+ * partial states that the call's last kernel merges; no initialisation; calls sharing one
+ * must not overlap on the GPU.  Launched as programmatic dependents of the preceding kernel.
+ */
+typedef struct {
+    const void* q;            /* [B,V,Hq,d] bf16 */
+    const void* k_cache;      /* [B,Hkv,T,d] of cache_dtype */
+    const void* v_cache;
+    const float* k_scale;     /* [B,Hkv,T] fp32, 8-bit caches only */
+    const float* v_scale;
+    sd_dtype cache_dtype;     /* SD_BF16, SD_I8 or SD_E4M3 */
+    const int32_t* qpos;      /* [B,V] device: last own row each query token sees, -1 none */
+    const int32_t* idx;       /* nullable [B,Hkv,n_idx] device: selected tokens or blocks */
+    const void* k_prefix;     /* [Hkv,P,d] bf16, NULL when P == 0 */
+    const void* v_prefix;
+    int B, V, Hq, Hkv, d, T, P, n_idx, block;
+    float scale;              /* softmax scale, e.g. 1/sqrt(d) */
+    void* out;                /* [B,V,Hq,d] of out_dtype, written */
+    sd_dtype out_dtype;       /* SD_F32 or SD_BF16 */
+    float* lse;               /* [B,V,Hq] fp32, written */
+    int32_t* err_word;        /* nullable device int32 */
+    void* workspace;          /* device scratch of workspace_bytes */
+    size_t workspace_bytes;
+} sd_cache_attend_args;
+
+size_t sd_cache_attend_workspace_bytes(const sd_cache_attend_args* args);
+sd_status sd_cache_attend(const sd_cache_attend_args* args, void* stream);
+
+/*
+ * sd_verify_drafts -- which drafted tokens the target accepts, and the token that follows.
+ * [DHiSparse] "Metodologia" (a verify step checks several drafted tokens at once); the rule is
+ * speculative sampling, with the random numbers as inputs.  Per sequence b with n = count[b]
+ * drafts (count NULL: V; clamped to [0, V]):
+ *     accepted[b] = a = the first i < n without u[b,i] * q[b,i,x_i] < p[b,i,x_i], or n
+ *                       (x_i = draft[b,i]; a draft outside [0, N) is not accepted and sets
+ *                       SD_DEVERR_INDEX);
+ *     r_t = max(p[b,a,t] - q[b,a,t], 0) when a < n (p[b,a,t] where that is zero for all t),
+ *           p[b,n,t] when a == n;
+ *     next = the lowest t with sum_{s<=t} r_s > u_next[b] * sum_s r_s  (-1 for a row of zeros);
+ *     tokens[b,:] = x_0 .. x_{a-1}, next, then -1.
+ * q NULL: drafts proposed with certainty (a draft by lookup): q is 1 at x_i and 0 elsewhere.
+ * p [B,V+1,N] and q [B,V,N] of dtype (F32, BF16 or F16): the target's and the draft's
+ * probabilities, within [0, 1], each row summing to less than 256 (they need not be
+ * normalised); draft [B,V] int32, u [B,V] and u_next [B] fp32 in [0, 1); tokens [B,V+1] and
+ * accepted [B] int32 (written).  The comparison is exact; the cumulative sums are exact sums
+ * of the weights in units of 2^-56, so the result depends on no order of additions.
+ * Limits: V <= 1024, 1 <= N <= 2^24.  Launched as a programmatic dependent of the preceding kernel.
+ */
+sd_status sd_verify_drafts(const void* p, const void* q, sd_dtype dtype, const int32_t* draft, const float* u,
+                           const float* u_next, const int32_t* count, int B, int V, int N, int32_t* tokens,
+                           int32_t* accepted, int32_t* err_word, void* stream);
 
 #ifdef __cplusplus
 }

@@ -18,7 +18,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libsdgqa.so")
 
 SD_OK, SD_ERR_INVALID_ARG, SD_ERR_UNSUPPORTED, SD_ERR_CUDA = 0, 1, 2, 3
-SD_F32, SD_BF16, SD_F16 = 0, 1, 2
+SD_F32, SD_BF16, SD_F16, SD_I8, SD_E4M3 = 0, 1, 2, 3, 4
 SD_DEVERR_INDEX, SD_DEVERR_SLOT, SD_DEVERR_TIMEOUT = 0x1, 0x2, 0x4
 
 # Every symbol include/sd.h declares (checked by the tests against the built library).
@@ -29,7 +29,8 @@ EXPORTS = (
     "sd_quantize_rows_int8", "sd_gather_attend_noalloc", "sd_select_attend", "sd_window_count",
     "sd_window_max", "sd_window_union", "sd_index_score_heads", "sd_stage_host_rows", "sd_ring_append",
     "sd_promote_rows_workspace_bytes", "sd_promote_rows", "sd_promote_staged_rows_workspace_bytes",
-    "sd_promote_staged_rows", "sd_decode_step_workspace_bytes", "sd_decode_step",
+    "sd_promote_staged_rows", "sd_decode_step_workspace_bytes", "sd_decode_step", "sd_q8_append",
+    "sd_cache_attend_workspace_bytes", "sd_cache_attend", "sd_verify_drafts",
 )
 
 
@@ -68,6 +69,31 @@ class sd_decode_step_args(ctypes.Structure):
         ("scores", ctypes.c_void_p), ("idx", ctypes.c_void_p), ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p),
         ("err_word", ctypes.c_void_p), ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
         ("lag", ctypes.c_int), ("wait_limit_ns", ctypes.c_longlong),
+    ]
+
+
+class sd_q8_append_args(ctypes.Structure):
+    _fields_ = [
+        ("k_new", ctypes.c_void_p), ("v_new", ctypes.c_void_p), ("dtype", ctypes.c_int),
+        ("B", ctypes.c_int), ("Hkv", ctypes.c_int), ("n", ctypes.c_int), ("d", ctypes.c_int), ("T", ctypes.c_int),
+        ("k_stride_b", ctypes.c_longlong), ("k_stride_h", ctypes.c_longlong), ("k_stride_n", ctypes.c_longlong),
+        ("v_stride_b", ctypes.c_longlong), ("v_stride_h", ctypes.c_longlong), ("v_stride_n", ctypes.c_longlong),
+        ("pos0", ctypes.c_void_p), ("count", ctypes.c_void_p), ("code_dtype", ctypes.c_int),
+        ("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+        ("v_scale", ctypes.c_void_p), ("err_word", ctypes.c_void_p),
+    ]
+
+
+class sd_cache_attend_args(ctypes.Structure):
+    _fields_ = [
+        ("q", ctypes.c_void_p), ("k_cache", ctypes.c_void_p), ("v_cache", ctypes.c_void_p),
+        ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p), ("cache_dtype", ctypes.c_int),
+        ("qpos", ctypes.c_void_p), ("idx", ctypes.c_void_p), ("k_prefix", ctypes.c_void_p),
+        ("v_prefix", ctypes.c_void_p), ("B", ctypes.c_int), ("V", ctypes.c_int), ("Hq", ctypes.c_int),
+        ("Hkv", ctypes.c_int), ("d", ctypes.c_int), ("T", ctypes.c_int), ("P", ctypes.c_int),
+        ("n_idx", ctypes.c_int), ("block", ctypes.c_int), ("scale", ctypes.c_float), ("out", ctypes.c_void_p),
+        ("out_dtype", ctypes.c_int), ("lse", ctypes.c_void_p), ("err_word", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
     ]
 
 
@@ -117,6 +143,11 @@ def lib() -> ctypes.CDLL:
         L.sd_decode_step_workspace_bytes.argtypes = [ctypes.POINTER(sd_decode_step_args)]
         L.sd_decode_step_workspace_bytes.restype = Z
         L.sd_decode_step.argtypes = [ctypes.POINTER(sd_decode_step_args), P]
+        L.sd_q8_append.argtypes = [ctypes.POINTER(sd_q8_append_args), P]
+        L.sd_cache_attend_workspace_bytes.argtypes = [ctypes.POINTER(sd_cache_attend_args)]
+        L.sd_cache_attend_workspace_bytes.restype = Z
+        L.sd_cache_attend.argtypes = [ctypes.POINTER(sd_cache_attend_args), P]
+        L.sd_verify_drafts.argtypes = [P, P, I, P, P, P, P, I, I, I, P, P, P, P]
         L.sd_stage_host_rows.restype = I
         L.sd_select_attend.restype = I
         for name in ("sd_index_score", "sd_block_pool", "sd_topk", "sd_gather_attend",
@@ -604,6 +635,186 @@ def decode_step(q_idx, keys, q, k_cache, v_cache, k, workspace=None, stream=None
     return scores, idx, out, lse
 
 
+def _same_device(**tensors):
+    """Contiguous tensors of the current CUDA device (None: left out), each of the given
+    (tensor, dtype(s), shape); raises for any that is not."""
+    for name, (t, dtypes, shape) in tensors.items():
+        if t is None:
+            continue
+        _dev(t, name)
+        if t.device.index != torch.cuda.current_device():
+            raise ValueError(f"{name} is on {t.device}, not on the current device")
+        if t.dtype not in (dtypes if isinstance(dtypes, tuple) else (dtypes,)):
+            raise TypeError(f"{name} has dtype {t.dtype}")
+        if tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name} must have shape {list(shape)}, not {list(t.shape)}")
+
+
+_CODE_DTYPES = {torch.int8: SD_I8, torch.float8_e4m3fn: SD_E4M3}
+
+
+def q8_cache(B: int, Hkv: int, T: int, d: int, dtype: torch.dtype = torch.int8, device="cuda") -> tuple:
+    """An empty 8-bit cache: (k_codes, v_codes [B,Hkv,T,d] of dtype (torch.int8 or
+    torch.float8_e4m3fn), k_scale, v_scale [B,Hkv,T] fp32), all zero."""
+    if dtype not in _CODE_DTYPES:
+        raise TypeError("codes are torch.int8 or torch.float8_e4m3fn")
+    k, v = (torch.zeros((B, Hkv, T, d), dtype=torch.int8, device=device).view(dtype) for _ in range(2))
+    ks, vs = (torch.zeros((B, Hkv, T), dtype=torch.float32, device=device) for _ in range(2))
+    return k, v, ks, vs
+
+
+def make_q8_append_args(k_new, v_new, k_codes, v_codes, k_scale, v_scale, pos0, count=None,
+                        err_word=None) -> sd_q8_append_args:
+    """Fill an sd_q8_append_args: k_new/v_new [B,Hkv,n,d] (float32, bfloat16 or float16, rows
+    contiguous, any strides of 16 bytes, e.g. a projection's [B,n,Hkv,d] transposed), the cache
+    of q8_cache, pos0 [B] int32 and optionally count [B] int32."""
+    B, Hkv, n, d = k_new.shape
+    T = k_codes.shape[2]
+    for name, t in (("k_new", k_new), ("v_new", v_new)):
+        if not t.is_cuda or t.device.index != torch.cuda.current_device():
+            raise ValueError(f"{name} must be a tensor on the current CUDA device")
+        if tuple(t.shape) != (B, Hkv, n, d) or t.dtype != k_new.dtype:
+            raise ValueError("k_new and v_new must have one shape [B,Hkv,n,d] and dtype")
+        if t.stride(3) != 1 and d > 1:
+            raise ValueError(f"{name}: the elements of a row must be contiguous")
+    if k_codes.dtype not in _CODE_DTYPES:
+        raise TypeError("codes are torch.int8 or torch.float8_e4m3fn")
+    _same_device(k_codes=(k_codes, k_codes.dtype, (B, Hkv, T, d)), v_codes=(v_codes, k_codes.dtype, (B, Hkv, T, d)),
+                 k_scale=(k_scale, torch.float32, (B, Hkv, T)), v_scale=(v_scale, torch.float32, (B, Hkv, T)),
+                 pos0=(pos0, torch.int32, (B,)), count=(count, torch.int32, (B,)),
+                 err_word=(err_word, torch.int32, (1,)))
+    a = sd_q8_append_args()
+    a.k_new, a.v_new, a.dtype = k_new.data_ptr(), v_new.data_ptr(), _dtype_code(k_new)
+    a.B, a.Hkv, a.n, a.d, a.T = B, Hkv, n, d, T
+    # a dimension of one element may have any stride: 0 says that it is not used
+    ks, vs = ([s if size > 1 else 0 for s, size in zip(t.stride(), t.shape)] for t in (k_new, v_new))
+    a.k_stride_b, a.k_stride_h, a.k_stride_n = ks[:3]
+    a.v_stride_b, a.v_stride_h, a.v_stride_n = vs[:3]
+    a.pos0 = pos0.data_ptr()
+    a.count = count.data_ptr() if count is not None else None
+    a.code_dtype = _CODE_DTYPES[k_codes.dtype]
+    a.k_codes, a.v_codes = k_codes.data_ptr(), v_codes.data_ptr()
+    a.k_scale, a.v_scale = k_scale.data_ptr(), v_scale.data_ptr()
+    a.err_word = err_word.data_ptr() if err_word is not None else None
+    return a
+
+
+def sd_q8_append(k_new, v_new, k_codes, v_codes, k_scale, v_scale, pos0, count=None, err_word=None,
+                 stream=None) -> None:
+    """Quantises the new rows into the 8-bit cache at rows pos0[b] + i (see make_q8_append_args)."""
+    a = make_q8_append_args(k_new, v_new, k_codes, v_codes, k_scale, v_scale, pos0, count, err_word)
+    _check(lib().sd_q8_append(ctypes.byref(a), _stream(stream)), "sd_q8_append")
+
+
+def make_cache_attend_args(q, k_cache, v_cache, qpos, *, k_scale=None, v_scale=None, idx=None, block=1, k_prefix=None,
+                           v_prefix=None, scale=None, out=None, lse=None, out_dtype=torch.float32,
+                           err_word=None) -> tuple:
+    """Fill an sd_cache_attend_args from tensors; returns (args, out, lse).  q [B,V,Hq,d]
+    bfloat16; k_cache/v_cache [B,Hkv,T,d] bfloat16, or int8 / float8_e4m3fn with k_scale/v_scale
+    [B,Hkv,T]; qpos [B,V] int32; idx [B,Hkv,n_idx] int32 tokens or blocks; k_prefix/v_prefix
+    [Hkv,P,d] bfloat16.  The workspace is set separately (cache_attend_workspace)."""
+    B, V, Hq, d = q.shape
+    Hkv, T = k_cache.shape[1], k_cache.shape[2]
+    eight = k_cache.dtype in _CODE_DTYPES
+    if not eight and k_cache.dtype != torch.bfloat16:
+        raise TypeError("the cache must be bfloat16, int8 or float8_e4m3fn")
+    if eight and (k_scale is None or v_scale is None):
+        raise ValueError("an 8-bit cache needs k_scale and v_scale")
+    if (k_prefix is None) != (v_prefix is None):
+        raise ValueError("k_prefix and v_prefix go together")
+    P = k_prefix.shape[1] if k_prefix is not None else 0
+    if out is None:
+        out = torch.empty((B, V, Hq, d), dtype=out_dtype, device=q.device)
+    if lse is None:
+        lse = torch.empty((B, V, Hq), dtype=torch.float32, device=q.device)
+    n_idx = idx.shape[-1] if idx is not None else 0
+    scales = (B, Hkv, T)
+    _same_device(q=(q, torch.bfloat16, (B, V, Hq, d)), k_cache=(k_cache, k_cache.dtype, (B, Hkv, T, d)),
+                 v_cache=(v_cache, k_cache.dtype, (B, Hkv, T, d)), k_scale=(k_scale, torch.float32, scales),
+                 v_scale=(v_scale, torch.float32, scales), qpos=(qpos, torch.int32, (B, V)),
+                 idx=(idx, torch.int32, (B, Hkv, n_idx)), k_prefix=(k_prefix, torch.bfloat16, (Hkv, P, d)),
+                 v_prefix=(v_prefix, torch.bfloat16, (Hkv, P, d)),
+                 out=(out, (torch.float32, torch.bfloat16), (B, V, Hq, d)), lse=(lse, torch.float32, (B, V, Hq)),
+                 err_word=(err_word, torch.int32, (1,)))
+    a = sd_cache_attend_args()
+    a.q, a.k_cache, a.v_cache, a.qpos = q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), qpos.data_ptr()
+    if eight:
+        a.k_scale, a.v_scale = k_scale.data_ptr(), v_scale.data_ptr()
+    a.cache_dtype = _CODE_DTYPES[k_cache.dtype] if eight else SD_BF16
+    if P > 0:
+        a.k_prefix, a.v_prefix = k_prefix.data_ptr(), v_prefix.data_ptr()
+    if n_idx > 0:
+        a.idx = idx.data_ptr()
+    elif idx is not None:
+        raise ValueError("idx must select at least one entry")
+    a.B, a.V, a.Hq, a.Hkv, a.d, a.T, a.P, a.n_idx, a.block = B, V, Hq, Hkv, d, T, P, n_idx, block
+    a.scale = 1.0 / math.sqrt(d) if scale is None else scale
+    a.out, a.lse = out.data_ptr(), lse.data_ptr()
+    a.out_dtype = SD_BF16 if out.dtype == torch.bfloat16 else SD_F32
+    a.err_word = err_word.data_ptr() if err_word is not None else None
+    return a, out, lse
+
+
+def sd_cache_attend_workspace_bytes(args: sd_cache_attend_args) -> int:
+    return lib().sd_cache_attend_workspace_bytes(ctypes.byref(args))
+
+
+def cache_attend_workspace(args: sd_cache_attend_args, device="cuda") -> torch.Tensor:
+    """A workspace for sd_cache_attend calls shaped like `args`, set into args."""
+    n = max(256, sd_cache_attend_workspace_bytes(args))
+    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    args.workspace, args.workspace_bytes = ws.data_ptr(), n
+    return ws
+
+
+def sd_cache_attend(args: sd_cache_attend_args, stream=None) -> None:
+    """Runs one sd_cache_attend call described by `args` (see make_cache_attend_args; the
+    workspace must be set, e.g. by cache_attend_workspace)."""
+    _check(lib().sd_cache_attend(ctypes.byref(args), _stream(stream)), "sd_cache_attend")
+
+
+def cache_attend(q, k_cache, v_cache, qpos, workspace=None, stream=None, **kw):
+    """Convenience wrapper: builds the args, sizes a workspace if none is given, runs the call
+    and returns (out, lse)."""
+    a, out, lse = make_cache_attend_args(q, k_cache, v_cache, qpos, **kw)
+    need = sd_cache_attend_workspace_bytes(a)
+    if workspace is None or workspace.numel() * workspace.element_size() < need:
+        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
+    a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    sd_cache_attend(a, stream)
+    if stream is not None and hasattr(stream, "cuda_stream"):
+        workspace.record_stream(stream)  # a workspace made here may be freed before the stream is done
+    return out, lse
+
+
+def _verify_args(p, q, draft, u, u_next, tokens, accepted, count, err_word, stream) -> tuple:
+    B, V1, N = p.shape
+    V = V1 - 1
+    _same_device(p=(p, (torch.float32, torch.bfloat16, torch.float16), (B, V1, N)), q=(q, p.dtype, (B, V, N)),
+                 draft=(draft, torch.int32, (B, V)), u=(u, torch.float32, (B, V)), u_next=(u_next, torch.float32, (B,)),
+                 tokens=(tokens, torch.int32, (B, V1)), accepted=(accepted, torch.int32, (B,)),
+                 count=(count, torch.int32, (B,)), err_word=(err_word, torch.int32, (1,)))
+    return (_ptr(p), _ptr(q), _dtype_code(p), _ptr(draft), _ptr(u), _ptr(u_next), _ptr(count), B, V, N, _ptr(tokens),
+            _ptr(accepted), _ptr(err_word), _stream(stream))
+
+
+def sd_verify_drafts(p: torch.Tensor, q: Optional[torch.Tensor], draft: torch.Tensor, u: torch.Tensor,
+                     u_next: torch.Tensor, tokens: Optional[torch.Tensor] = None,
+                     accepted: Optional[torch.Tensor] = None, count: Optional[torch.Tensor] = None,
+                     err_word: Optional[torch.Tensor] = None, stream=None) -> tuple:
+    """(tokens [B,V+1] int32: the accepted drafts, the next token, then -1; accepted [B] int32)
+    from the target's probabilities p [B,V+1,N], the draft's q [B,V,N] of the same dtype (None:
+    drafts proposed with certainty), draft [B,V] int32 and the random numbers u [B,V], u_next
+    [B] fp32; count [B] int32: the drafts each sequence has."""
+    if tokens is None:
+        tokens = torch.empty(p.shape[:2], dtype=torch.int32, device=p.device)
+    if accepted is None:
+        accepted = torch.empty(p.shape[:1], dtype=torch.int32, device=p.device)
+    _check(lib().sd_verify_drafts(*_verify_args(p, q, draft, u, u_next, tokens, accepted, count, err_word, stream)),
+           "sd_verify_drafts")
+    return tokens, accepted
+
+
 class PreparedCall:
     """One C-ABI call with its arguments marshalled once: calling the object invokes the
     library function directly, with no per-call shape checks, pointer lookups or Python
@@ -655,3 +866,21 @@ def prepare_stage_host_rows(args: sd_attend_args, counter, stream=None) -> Prepa
 
 def prepare_decode_step(args: sd_decode_step_args, stream=None) -> PreparedCall:
     return PreparedCall("sd_decode_step", ctypes.byref(args), _stream(stream))
+
+
+def prepare_q8_append(k_new, v_new, k_codes, v_codes, k_scale, v_scale, pos0, count=None, err_word=None,
+                      stream=None) -> PreparedCall:
+    a = make_q8_append_args(k_new, v_new, k_codes, v_codes, k_scale, v_scale, pos0, count, err_word)
+    return PreparedCall("sd_q8_append", ctypes.byref(a), _stream(stream))
+
+
+def prepare_cache_attend(args: sd_cache_attend_args, workspace=None, stream=None) -> PreparedCall:
+    if workspace is not None:
+        args.workspace, args.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    return PreparedCall("sd_cache_attend", ctypes.byref(args), _stream(stream))
+
+
+def prepare_verify_drafts(p, q, draft, u, u_next, tokens, accepted, count=None, err_word=None,
+                          stream=None) -> PreparedCall:
+    return PreparedCall("sd_verify_drafts",
+                        *_verify_args(p, q, draft, u, u_next, tokens, accepted, count, err_word, stream))

@@ -1,0 +1,382 @@
+// prefix_attend.cu -- the prefix that a serving batch shares, attended once for all sequences on
+// the 5th-generation tensor cores: the part of sd_cache_attend over k_prefix/v_prefix.
+//
+// "Esparsidade de Contexto no Tempo de Inferencia" (gist.science summary), sec. 2 (exact softmax);
+// Adaptive DHiSparse (news page), "Metodologia" (query tokens share each fetched row: here the
+// rows of all sequences' query tokens).
+//
+// Mathematics.  The query rows of one KV head, M = B*V*G of them, form one matrix: S = Q K^T, P =
+// 2^(S c - m), O = P V with the softmax kept online per row (m, l), as in flash attention.  The
+// sequences' rows are split over CTAs in pairs of 128-row tiles, the prefix into splits; every
+// (rows, split) leaves its (m, l, O), which the call's merge kernel joins with the states of
+// the sequences' own rows.
+//
+// Bound: for up to about 256 rows a KV head HBM (a key tile is read once for both row tiles),
+// beyond it the tensor cores and the exponentials.  One CTA an SM; per key tile of 128 and row tile
+// t = 0, 1: S_t (128 x 128 fp32 accumulators in TMEM) by d/16 MMAs, softmax by warpgroup t (one
+// thread a row: no shuffles), P_t back into the TMEM columns S_t held (two bf16 parts of 64
+// columns each, or one), O_t += P_t V with P from TMEM and V as it lies in memory (MN-major).
+// The MMA warp alternates the tiles, so the tensor cores work on one while the other's softmax
+// runs.  O_t is rescaled only when a row's maximum has grown by more than 2^8 since the last time
+// (weights stay below 2^8; the quotient O / l does not change), which is rare after the first tiles.
+// TMEM: S_0, S_1 (128 columns each), O_0, O_1 (d each).  Shared memory: 2 Q tiles, 2 stages of K
+// and of V.  Every wait is bounded; a wait that runs out raises an abort flag, the copies and MMAs
+// in flight land, and the kernel frees its TMEM and returns.
+#include <cmath>
+
+#include "cache_attend.cuh"
+#include "step_tiles.cuh"
+#include "tc_common.cuh"
+
+namespace sd {
+namespace {
+
+constexpr int kPfKeys = 128;  // keys a tile
+constexpr int kPfRows = 128;  // query rows a tile
+constexpr int kPfProd = 8, kPfMma = 9;  // warps 0-3 and 4-7: softmax of row tiles 0 and 1
+constexpr int kPfThreads = 32 * 10;
+constexpr int kPfStages = 2;
+constexpr float kPfGrow = 8.f;  // the growth of a row's maximum (base 2) that O is rescaled at
+
+template <int D>
+struct PfLayout {
+    static constexpr int kAtoms = D / 64;
+    static constexpr int kAtom = 128 * 128;           // 128 rows of 64 bf16
+    static constexpr int kTile = kAtoms * kAtom;
+    static constexpr int oQ = 0;
+    static constexpr int oK = oQ + 2 * kTile;
+    static constexpr int oV = oK + kPfStages * kTile;
+    static constexpr int oBars = oV + kPfStages * kTile;
+    static constexpr int oMisc = oBars + 32 * 8;
+    static constexpr int kBytes = oMisc + 32 + 1024;  // slack for the 1024-byte alignment
+};
+
+struct PfParams {
+    float2* ml;
+    float* o;
+    int32_t* err;
+    int M, G, P, splits, pairs, tiles, row_tiles, bpt;
+    float scale_log2;
+    unsigned long long wait_ns;
+};
+
+template <int D, bool HILO>
+__global__ void __launch_bounds__(kPfThreads, 1)
+    prefix_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
+                  const __grid_constant__ CUtensorMap vmap, const PfParams p) {
+    using L = PfLayout<D>;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_addr(smem_raw);
+    uint8_t* sm = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
+    uint64_t* qfull = reinterpret_cast<uint64_t*>(sm + L::oBars);
+    uint64_t* kfull = qfull + 1;
+    uint64_t* kempty = kfull + kPfStages;
+    uint64_t* vfull = kempty + kPfStages;
+    uint64_t* vempty = vfull + kPfStages;
+    uint64_t* sfull = vempty + kPfStages;  // [2] S_t is in TMEM (and O_t += P_t V of the tile before is done)
+    uint64_t* pfull = sfull + 2;           // [2] P_t is in TMEM
+    uint64_t* ofull = pfull + 2;           // [2] the last O_t is done
+    uint64_t* drain = ofull + 2;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + L::oMisc);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + L::oMisc + 4);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int pair = (int)blockIdx.x % p.pairs, rest = (int)blockIdx.x / p.pairs;
+    const int split = rest % p.splits, kvh = rest / p.splits;
+    const int n0 = (int)((long)split * p.tiles / p.splits), n1 = (int)((long)(split + 1) * p.tiles / p.splits);
+    const int nt = n1 - n0;
+    const int nq = min(2, p.row_tiles - 2 * pair);  // row tiles of this CTA
+    const uint64_t lim = p.wait_ns;
+
+    if (tid == 0) {
+        mbar_init(qfull, 1);
+        for (int s = 0; s < kPfStages; ++s) {
+            mbar_init(&kfull[s], 1);
+            mbar_init(&kempty[s], 1);
+            mbar_init(&vfull[s], 1);
+            mbar_init(&vempty[s], 1);
+        }
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(&sfull[t], 1);
+            mbar_init(&pfull[t], 4);  // one arrival a softmax warp
+            mbar_init(&ofull[t], 1);
+        }
+        mbar_init(drain, 1);
+        *abort_flag = 0;
+        fence_mbarrier_init();
+    }
+    if (warp == kPfMma) tmem_alloc(tmem_slot, 512);
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem = *tmem_slot;
+    pdl_wait();  // q and the prefix may be the preceding kernels' results
+    pdl_launch_dependents();
+
+    int issued = 0;  // key tiles whose K and V the producer asked for
+    if (warp == kPfProd) {
+        if (lane == 0) {
+            const uint32_t qbytes = (uint32_t)(p.G * p.bpt) * 128u;
+            mbar_arrive_expect_tx(qfull, (uint32_t)nq * L::kAtoms * qbytes);
+            for (int t = 0; t < nq; ++t)
+#pragma unroll
+                for (int a = 0; a < L::kAtoms; ++a)
+                    tma_load_3d(sm + L::oQ + t * L::kTile + a * L::kAtom, &qmap, 64 * a, kvh * p.G,
+                                (2 * pair + t) * p.bpt, qfull);
+            for (int n = 0; n < nt; ++n) {
+                const int s = n % kPfStages;
+                const uint32_t ph = ((uint32_t)(n / kPfStages) & 1u) ^ 1u;
+                const int key = (n0 + n) * kPfKeys;
+                if (!ds_wait(&kempty[s], ph, abort_flag, lim)) {
+                    *abort_flag = 1;
+                    break;
+                }
+                mbar_arrive_expect_tx(&kfull[s], L::kTile);
+#pragma unroll
+                for (int a = 0; a < L::kAtoms; ++a)
+                    tma_load_3d(sm + L::oK + s * L::kTile + a * L::kAtom, &kmap, 64 * a, key, kvh, &kfull[s]);
+                issued = 2 * n + 1;
+                if (!ds_wait(&vempty[s], ph, abort_flag, lim)) {
+                    *abort_flag = 1;
+                    break;
+                }
+                mbar_arrive_expect_tx(&vfull[s], L::kTile);
+#pragma unroll
+                for (int a = 0; a < L::kAtoms; ++a)
+                    tma_load_3d(sm + L::oV + s * L::kTile + a * L::kAtom, &vmap, 64 * a, key, kvh, &vfull[s]);
+                issued = 2 * n + 2;
+            }
+        }
+    } else if (warp == kPfMma) {
+        if (lane == 0) {
+            constexpr uint32_t kIdS = umma_idesc_bf16_f32(kPfRows, kPfKeys);
+            constexpr uint32_t kIdO = umma_idesc_bf16_f32(kPfRows, D) | kUmmaBMnMajor;
+            const uint32_t base = smem_addr(sm);
+            auto scores = [&](int t, int n) {  // S_t = Q_t K_n^T
+                const uint32_t a0 = base + L::oQ + t * L::kTile, b0 = base + L::oK + (n % kPfStages) * L::kTile;
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                    const uint32_t off = (uint32_t)((k >> 2) * L::kAtom + (k & 3) * 32);
+                    umma_bf16(tmem + t * 128, umma_desc_k_sw128(a0 + off), umma_desc_k_sw128(b0 + off), kIdS,
+                              k > 0 ? 1u : 0u);
+                }
+                umma_commit(&sfull[t]);
+            };
+            auto output = [&](int t, int n) {  // O_t += P_t V_n
+                const uint32_t b0 = base + L::oV + (n % kPfStages) * L::kTile;
+                const uint32_t o = tmem + 256 + t * 128, a = tmem + t * 128;
+#pragma unroll
+                for (int k = 0; k < kPfKeys / 16; ++k) {
+                    const uint64_t bd = umma_desc_mn_sw128(b0 + k * 2048, L::kAtom);
+                    umma_bf16_ta(o, a + 8 * k, bd, kIdO, (n > 0 || k > 0) ? 1u : 0u);
+                    if (HILO) umma_bf16_ta(o, a + 64 + 8 * k, bd, kIdO, 1u);
+                }
+            };
+            bool ok = ds_wait(qfull, 0u, abort_flag, lim) && ds_wait(&kfull[0], 0u, abort_flag, lim);
+            if (ok) {
+                tc_fence_after_sync();
+                for (int t = 0; t < nq; ++t) scores(t, 0);
+                umma_commit(&kempty[0]);
+            }
+            for (int n = 0; ok && n < nt; ++n) {
+                const uint32_t ph = (uint32_t)(n / kPfStages) & 1u;
+                const uint32_t phn = (uint32_t)((n + 1) / kPfStages) & 1u;
+                ok = ds_wait(&vfull[n % kPfStages], ph, abort_flag, lim);
+                if (ok && n + 1 < nt) ok = ds_wait(&kfull[(n + 1) % kPfStages], phn, abort_flag, lim);
+                for (int t = 0; ok && t < nq; ++t) {
+                    ok = ds_wait(&pfull[t], (uint32_t)n & 1u, abort_flag, lim);
+                    if (!ok) break;
+                    tc_fence_after_sync();
+                    output(t, n);
+                    if (n + 1 < nt) scores(t, n + 1);
+                    else umma_commit(&ofull[t]);
+                }
+                if (!ok) break;
+                umma_commit(&vempty[n % kPfStages]);
+                if (n + 1 < nt) umma_commit(&kempty[(n + 1) % kPfStages]);
+            }
+            if (!ok) {  // let the MMAs in flight finish before their operands and TMEM go
+                *abort_flag = 1;
+                umma_commit(drain);
+                mbar_wait(drain, 0u, lim);
+            }
+        }
+    } else if ((warp >> 2) < nq) {
+        const int t = warp >> 2, quarter = warp & 3;
+        const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+        const uint32_t ts = tmem + lanes + t * 128, to = tmem + lanes + 256 + t * 128;
+        const int r = quarter * 32 + lane;  // this thread's row of the tile
+        const bool mine = r < p.G * p.bpt;
+        float m = -INFINITY, l = 0.f;
+        bool ok = true;
+        for (int n = 0; n < nt; ++n) {
+            if (!warp_wait(&sfull[t], (uint32_t)n & 1u, const_cast<volatile int*>(abort_flag), lim)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after_sync();
+            uint32_t s[128];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tmem_ld32_nowait(ts + 32 * c, s + 32 * c);
+            tmem_wait_ld();
+            const int valid = p.P - (n0 + n) * kPfKeys;  // keys of the tile within the prefix
+            if (valid < kPfKeys) {
+#pragma unroll
+                for (int i = 0; i < kPfKeys; ++i)
+                    if (i >= valid) s[i] = 0xff800000u;  // -inf
+            }
+            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int i = 0; i < kPfKeys; ++i) mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(s[i]));
+            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
+            // (rows past the tile's query rows hold whatever shared memory held: left alone)
+            const float grown = mine && top > m + kPfGrow ? top : m;
+            if (n == 0) {
+                m = top;
+            } else if (__any_sync(0xffffffffu, grown != m)) {
+                const float f = fast_exp2(m - grown);
+                l *= f;
+                m = grown;
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t o[32];
+                    tmem_ld32_nowait(to + 32 * c, o);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                    tmem_st16(to + 32 * c, o);
+                    tmem_st16(to + 32 * c + 16, o + 16);
+                }
+            }
+            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                uint32_t hi[16], lo[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float x = fast_exp2(fmaf(__uint_as_float(s[32 * c + 2 * i]), p.scale_log2, -m));
+                    const float y = fast_exp2(fmaf(__uint_as_float(s[32 * c + 2 * i + 1]), p.scale_log2, -m));
+                    sum[(2 * i) & 3] += x;
+                    sum[(2 * i + 1) & 3] += y;
+                    if constexpr (HILO)
+                        split_bf16x2(x, y, hi[i], lo[i]);
+                    else
+                        hi[i] = pack_bf16x2(x, y);
+                }
+                tmem_st16(ts + 16 * c, hi);
+                if constexpr (HILO) tmem_st16(ts + 64 + 16 * c, lo);
+            }
+            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            tmem_wait_st();
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&pfull[t]);
+        }
+        if (ok) ok = warp_wait(&ofull[t], 0u, const_cast<volatile int*>(abort_flag), lim);
+        if (ok) {
+            tc_fence_after_sync();
+            const long row = (long)(2 * pair + t) * p.G * p.bpt + r;
+            const bool store = mine && row < p.M;
+            const size_t at = ((size_t)kvh * p.splits + split) * p.M + (store ? row : 0);
+            if (store) p.ml[at] = make_float2(m, l);
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+                uint32_t o[32];
+                tmem_ld32_nowait(to + 32 * c, o);
+                tmem_wait_ld();
+                if (store) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        reinterpret_cast<uint4*>(p.o + at * D + 32 * c)[i] =
+                            make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                }
+            }
+            tc_fence_before_sync();
+        }
+    }
+    __syncthreads();
+    if (*abort_flag) {
+        if (tid == 32 * kPfProd) {  // let the copies in flight land
+            mbar_wait(qfull, 0u, lim);
+            for (int i = max(0, issued - 2 * kPfStages); i < issued; ++i) {
+                const int n = i >> 1;
+                mbar_wait((i & 1 ? vfull : kfull) + n % kPfStages, (uint32_t)(n / kPfStages) & 1u, lim);
+            }
+            report(p.err, SD_DEVERR_TIMEOUT);
+        }
+        __syncthreads();
+    }
+    if (warp == kPfMma) {
+        tc_fence_after_sync();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+struct PfShape {
+    int bpt, row_tiles, pairs, tiles;
+};
+PfShape pf_shape(const sd_cache_attend_args* a) {
+    PfShape s{};
+    const int G = a->Hq / a->Hkv;
+    s.bpt = kPfRows / G;  // (sequence, query token) entries of a row tile
+    s.row_tiles = (int)(((long)a->B * a->V + s.bpt - 1) / s.bpt);
+    s.pairs = (s.row_tiles + 1) / 2;
+    s.tiles = (a->P + kPfKeys - 1) / kPfKeys;
+    return s;
+}
+
+}  // namespace
+
+// Splits of the prefix: the count whose slowest SM has the least to do, at 4 key tiles' time for what a
+// CTA does besides its tiles.
+int prefix_splits(const sd_cache_attend_args* a) {
+    const PfShape s = pf_shape(a);
+    const long units = (long)a->Hkv * s.pairs, sms = num_sms();
+    int best = 1;
+    long cost = -1;
+    for (int n = 1; n <= s.tiles && (n == 1 || units * n <= 4 * sms); ++n) {
+        const long c = ((units * n + sms - 1) / sms) * ((s.tiles + n - 1) / n + 4);
+        if (cost < 0 || c < cost) {
+            cost = c;
+            best = n;
+        }
+    }
+    return best;
+}
+
+sd_status prefix_launch(const sd_cache_attend_args* a, int splits, const CaWorkspace& w, cudaStream_t st) {
+    const char* who = "sd_cache_attend";
+    const PfShape s = pf_shape(a);
+    CUtensorMap qmap, kmap, vmap;
+    if (!make_tensor_map_3d(&qmap, a->q, (uint64_t)a->B * a->V, (uint64_t)a->Hq, a->d, s.bpt, a->Hq / a->Hkv) ||
+        !make_tensor_map_3d(&kmap, a->k_prefix, (uint64_t)a->Hkv, (uint64_t)a->P, a->d, 1, kPfKeys) ||
+        !make_tensor_map_3d(&vmap, a->v_prefix, (uint64_t)a->Hkv, (uint64_t)a->P, a->d, 1, kPfKeys)) {
+        set_error("%s: cuTensorMapEncodeTiled failed", who);
+        return SD_ERR_CUDA;
+    }
+    PfParams p{};
+    p.ml = w.pre_ml;
+    p.o = w.pre_o;
+    p.err = a->err_word;
+    p.G = a->Hq / a->Hkv;
+    p.M = a->B * a->V * p.G;
+    p.P = a->P;
+    p.splits = splits;
+    p.pairs = s.pairs;
+    p.tiles = s.tiles;
+    p.row_tiles = s.row_tiles;
+    p.bpt = s.bpt;
+    p.scale_log2 = a->scale * 1.44269504088896340736f;
+    p.wait_ns = (unsigned long long)kWaitDeadlineNs;
+    const bool hilo = a->out_dtype == SD_F32;
+    auto kern = a->d == 128 ? (hilo ? prefix_kernel<128, true> : prefix_kernel<128, false>)
+                            : (hilo ? prefix_kernel<64, true> : prefix_kernel<64, false>);
+    const int bytes = a->d == 128 ? PfLayout<128>::kBytes : PfLayout<64>::kBytes;
+    SD_CUDA_CHECK(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes),
+                  "sd_cache_attend: cudaFuncSetAttribute");
+    SD_CUDA_CHECK(launch_pdl(kern, dim3((unsigned)(a->Hkv * s.pairs * splits)), dim3(kPfThreads), (size_t)bytes, st, qmap,
+                             kmap, vmap, p),
+                  "sd_cache_attend: prefix launch");
+    return launch_status(who);
+}
+
+}  // namespace sd
