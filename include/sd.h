@@ -628,7 +628,7 @@ sd_status sd_cache_attend(const sd_cache_attend_args* args, void* stream);
  * probabilities, within [0, 1], each row summing to less than 256 (they need not be
  * normalised); draft [B,V] int32, u [B,V] and u_next [B] fp32 in [0, 1); tokens [B,V+1] and
  * accepted [B] int32 (written).  The comparison is exact; the cumulative sums are exact sums
- * of the weights in units of 2^-56, so the result depends on no order of additions.
+ * of the probabilities rounded to multiples of 2^-45, so the result depends on no order of additions.
  * Limits: V <= 1024, 1 <= N <= 2^24.  Launched as a programmatic dependent of the preceding kernel.
  */
 sd_status sd_verify_drafts(const void* p, const void* q, sd_dtype dtype, const int32_t* draft, const float* u,

@@ -9,23 +9,31 @@
 // fetched row).
 //
 // Mathematics.  z = scale * ks_t * (q . c_t), p = 2^(z log2 e - m), out = sum p vs_t c'_t / sum p.
-// The codes enter the tensor cores as they are (int8 and e4m3 values are exact in fp16, e4m3
-// scaled by 2^-8), the row scales multiply the logit and the weight in fp32.  The query row is
-// scaled by a power of two to [1, 2) before it becomes fp16, which keeps 24 bits below its largest
-// element.  The weight that multiplies a V row is p * vs_t, and its range is that of the scales: it is
-// kept relative to a second running maximum, over z + exponent(vs_t), whose weights reach up to
-// 2^15 in fp16 (so a weight 2^-39 times the largest still counts); with SD_F32 output
-// as a sum of two fp16 numbers (22 bits), with SD_BF16 output as one (11 bits, below the
-// output's own 8).  A bf16 cache uses bf16 operands, weights in two parts or one likewise.
+// The codes enter the tensor cores as they are (int8 and e4m3 values are exact in fp16), the row
+// scales multiply the logit and the weight in fp32.  The query row is scaled by a power of two
+// to [1, 2) before it becomes fp16, which keeps 24 bits below its largest element.  The weight that
+// multiplies a V row is p * vs_t, and its range is that of the scales: it is kept relative to a
+// second maximum, over z + log2(vs_t), whose weights are 2^10 in fp16 (and up to 2^15, see
+// below; a weight 2^-34 times the largest still counts); with SD_F32 output as a sum of two
+// fp16 numbers (22 bits), with SD_BF16 output as one (11 bits, below the output's own 8).  A bf16
+// cache uses bf16 operands, weights in two parts or one likewise.
+// The maxima need not be exact, only near: they move when a step's weights would pass 2^4 times
+// what they stand for, which one vote a step finds out; until then no value crosses lanes.
+// The tensor cores cut what they add to a sum (2^-24 of it), so SD_F32 output folds the
+// accumulators into fp32 sums in shared memory every 32 steps (a 131072-row cache: 1.5e-5 of
+// error in the output without, 3e-6 with).
 //
-// Bound: HBM.  So that nothing but the loads takes time, the rows go from global memory straight into
-// registers in the operand layout of mma.sync m16n8k16, with no shared memory: the contraction
-// over d may run in any order, so a lane takes 16 neighbouring bytes of its K rows as its elements
-// of four k-steps (the query fragments are permuted alike), and the output columns may be in
-// any order, so it takes 16 neighbouring columns of its four V rows.  Every load instruction then
-// covers whole 64- or 128-byte lines.  S^T = K Q^T and O^T = V^T P^T put the 16 rows of a step on
-// the M side and 8 query rows on the N side.  While a step is computed the next one's rows are on
-// their way (2 x 2 KB a warp, 12 to 16 warps an SM).
+// Bound: HBM; for more than 16 query rows the tensor cores' mma.sync rate comes close (8 cycles an
+// instruction: 174 us against 163 us of loads for 4 x 131072 int8 rows and 32 query rows in two-part
+// weights).  So that little but the loads takes time, the rows go from global memory straight
+// into registers in the operand layout of mma.sync m16n8k16, with no shared memory: the
+// contraction over d may run in any order, so a lane takes 16 neighbouring bytes of its K rows as
+// its elements of four k-steps (the query fragments are permuted alike), and the output columns
+// may be in any order, so it takes 16 neighbouring columns of its four V rows.  Every load
+// instruction then covers whole 64- or 128-byte lines.  S^T = K Q^T and O^T = V^T P^T put the 16
+// rows of a step on the M side and 8 query rows on the N side (NQ = 1, 2 or 4 of them in one warp:
+// a row's codes are widened once for all).  The next step's K rows are fetched as soon as this
+// one's are used, V rows likewise, so each load has half a step and the other warps to hide behind.
 //
 // Work: units of 64 rows of one (sequence, KV head), in order, cut into equal runs, one a CTA
 // (all resident at once), whatever the sequences' lengths.  A CTA's run covers one or more
@@ -64,9 +72,8 @@ enum { kBf16 = 0, kInt8 = 1, kE4m3 = 2 };
 
 // ------------------------------------------------------------------ operands
 
-// Bytes 0, 1 (hi: 2, 3) of w as two fp16: int8 from w ^ 0x80808080 (1024 + code + 128 as bits), e4m3 as
-// value * 2^-8 (its exponent and mantissa bits moved into fp16's; exact, subnormals too; a NaN code
-// gives 480 * 2^-8, never a NaN).
+// Bytes 0, 1 (hi: 2, 3) of w as two fp16: int8 from w ^ 0x80808080 (1024 + code + 128 as bits),
+// e4m3 by the conversion instruction.
 template <int KIND>
 SD_DEVINL uint32_t widen(uint32_t w, bool hi) {
     if constexpr (KIND == kInt8) {
@@ -75,8 +82,10 @@ SD_DEVINL uint32_t widen(uint32_t w, bool hi) {
         const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&t), *reinterpret_cast<const __half2*>(&c));
         return *reinterpret_cast<const uint32_t*>(&r);
     } else {
-        const uint32_t t = __byte_perm(w, 0u, hi ? 0x3424 : 0x1404);
-        return (t & 0x80008000u) | ((t >> 1) & 0x3f803f80u);
+        uint32_t r;
+        const uint16_t b = (uint16_t)(hi ? w >> 16 : w);
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(b));
+        return r;
     }
 }
 template <int KIND>
@@ -89,21 +98,20 @@ SD_DEVINL uint32_t pack_f16x2(float lo, float hi) {
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// A pair of weights as one 16-bit operand word, and what is left of them as another.
-template <bool F16>
-SD_DEVINL uint32_t weight_word(float x0, float x1, uint32_t* lo) {
+// A pair of weights as one 16-bit operand word, and (HILO) what is left of them as another.
+template <bool F16, bool HILO>
+SD_DEVINL void weight_words(float x0, float x1, uint32_t& hi, uint32_t& lo) {
     if constexpr (F16) {
         const __half2 h = __floats2half2_rn(x0, x1);
-        if (lo != nullptr) {
+        hi = *reinterpret_cast<const uint32_t*>(&h);
+        if constexpr (HILO) {
             const float2 f = __half22float2(h);
-            *lo = pack_f16x2(x0 - f.x, x1 - f.y);
+            lo = pack_f16x2(x0 - f.x, x1 - f.y);
         }
-        return *reinterpret_cast<const uint32_t*>(&h);
+    } else if constexpr (HILO) {
+        split_bf16x2(x0, x1, hi, lo);
     } else {
-        uint32_t hi, l;
-        split_bf16x2(x0, x1, hi, l);
-        if (lo != nullptr) *lo = l;
-        return hi;
+        hi = pack_bf16x2(x0, x1);
     }
 }
 
@@ -115,30 +123,25 @@ SD_DEVINL void mma16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint3
         mma_bf16_16816(d, a0, a1, a2, a3, b0, b1);
 }
 
-// 16 bytes (or 8) of a row read once: past L1, as data that nothing else wants (a verify batch
-// of more than 16 query rows has two warps reading the same rows: they share them in L1).
 SD_DEVINL uint4 ld_row16(const uint8_t* p) { return __ldg(reinterpret_cast<const uint4*>(p)); }
 SD_DEVINL uint2 ld_row8(const uint8_t* p) { return __ldg(reinterpret_cast<const uint2*>(p)); }
 
-// ------------------------------------------------------------------ one step's rows
-
-// 16 rows of K and V as this lane holds them.
+// What a lane holds of a step's 16 rows.
 template <int KIND, int D>
 struct Rows {
     static constexpr int kEs = KIND == kBf16 ? 2 : 1;
-    static constexpr int kKc = D * kEs / 64;  // 16-byte pieces of a K row a lane holds
-    static constexpr int kVw = D * kEs / 32;  // 32-bit words of a V row a lane holds
-    uint4 k[2][kKc];       // rows g8 and g8 + 8, bytes 64c + 16 t4 ..
-    uint32_t v[4][kVw];    // rows 2 t4, 2 t4 + 1, 2 t4 + 8, 2 t4 + 9, columns g8 * D/8 ..
+    static constexpr int kRow = D * kEs;      // bytes of a row
+    static constexpr int kKc = kRow / 64;     // 16-byte pieces of a K row a lane holds
+    static constexpr int kVw = kRow / 32;     // 32-bit words of a V row a lane holds
+    uint4 k[2][kKc];       // K rows g8 and g8 + 8, bytes 64c + 16 t4 ..
     float ks[2], vs[2];    // scales of rows g8 and g8 + 8
-    int pos[2];            // their positions (INT_MAX: not attended by any query)
+    uint32_t v[4][kVw];    // V rows 2 t4, 2 t4 + 1, 2 t4 + 8, 2 t4 + 9, columns g8 * D/8 ..
 
-    SD_DEVINL void load_k(int h, const uint8_t* row, int t4) {
+    SD_DEVINL void load_k(int h, const uint8_t* p) {  // p: the row's byte 16 t4
 #pragma unroll
-        for (int c = 0; c < kKc; ++c) k[h][c] = ld_row16(row + 64 * c + 16 * t4);
+        for (int c = 0; c < kKc; ++c) k[h][c] = ld_row16(p + 64 * c);
     }
-    SD_DEVINL void load_v(int r, const uint8_t* row, int g8) {
-        const uint8_t* p = row + g8 * (4 * kVw);
+    SD_DEVINL void load_v(int r, const uint8_t* p) {  // p: the row's column g8 * D/8
         if constexpr (kVw == 2) {
             const uint2 w = ld_row8(p);
             v[r][0] = w.x;
@@ -158,12 +161,18 @@ struct Rows {
 
 // ------------------------------------------------------------------ a warp's state
 
+constexpr float kNone = -1e30f;    // a maximum over no rows (finite: differences of it stay numbers)
+constexpr float kGrow = 4.f;       // how far (base 2) a weight may pass its maximum before that moves
+constexpr float kTopF16 = 10.f;    // log2 of the largest product weight when its maximum has just moved
+constexpr float kLimF16 = 32768.f; // the product weight at which it moves
+
 template <int D, int NQ>
 struct CaState {
-    float o[D / 16][NQ][4];   // O^T: columns g8 * D/8 + 2 md (+1: entries 2, 3) of query 8nq + 2t4 + e
-    float m[NQ][2], l[NQ][2]; // running max (base 2); this lane's share of the denominator
-    float m2[NQ][2];          // 8-bit: running max of logit + exponent of the V scale
-    SD_DEVINL void init() {
+    float o[D / 16][NQ][4];    // O^T: columns g8 * D/8 + 2 md (+1: entries 2, 3) of query 8nq + 2t4 + e
+    float m[NQ][2], l[NQ][2];  // maximum (base 2) and this lane's share of the denominator
+    float c[NQ][2];            // 8-bit: the product weight is p * vs * c (c = 2^(m - m2 + kTopF16), m2 the
+                               // maximum of logit + log2 vs)
+    SD_DEVINL void clear() {
 #pragma unroll
         for (int md = 0; md < D / 16; ++md)
 #pragma unroll
@@ -171,11 +180,16 @@ struct CaState {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) o[md][nq][e] = 0.f;
 #pragma unroll
+        for (int nq = 0; nq < NQ; ++nq) l[nq][0] = l[nq][1] = 0.f;
+    }
+    SD_DEVINL void init() {
+        clear();
+#pragma unroll
         for (int nq = 0; nq < NQ; ++nq)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                m[nq][e] = m2[nq][e] = -INFINITY;
-                l[nq][e] = 0.f;
+                m[nq][e] = kNone;
+                c[nq][e] = 0.f;
             }
     }
 };
@@ -185,14 +199,29 @@ SD_DEVINL float max_over_rows(float x) {  // over the lanes of the same t4
     x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
     return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
 }
+SD_DEVINL float sum_over_rows(float x) {
+    x += __shfl_xor_sync(0xffffffffu, x, 4);
+    x += __shfl_xor_sync(0xffffffffu, x, 8);
+    return x + __shfl_xor_sync(0xffffffffu, x, 16);
+}
 
-// One step: S^T = K Q^T, the online softmax over the rows at or below each query's limit, then
-// O^T += V^T P^T.  qs: each query's factor of the logit; lim: its last row (-1: none).
-template <int KIND, int D, int NQ, bool HILO>
-SD_DEVINL void ca_step(const Rows<KIND, D>& rw, const uint32_t (&qf)[D / 16][NQ][2], const float (&qs)[NQ][2],
-                       const int (&lim)[NQ][2], CaState<D, NQ>& st) {
+// The B fragments of the query rows, in registers or (two tiles and more) in shared memory.
+template <int D, int NQ>
+struct Queries {
+    static constexpr bool kShared = NQ >= 2;
+    uint32_t f[kShared ? 1 : D / 16][kShared ? 1 : NQ][2];
+    const uint2* sh;  // [D/16][NQ][32]
+    float qs[NQ][2];  // each query's factor of the logit (with the shared prefix's base 2)
+    SD_DEVINL uint2 at(int ks, int nq, int lane) const {
+        if constexpr (kShared) return sh[(ks * NQ + nq) * 32 + lane];
+        return make_uint2(f[ks][nq][0], f[ks][nq][1]);
+    }
+};
+
+// S^T = K Q^T of a step: s[nq][2h + e] of row g8 + 8h and query 8nq + 2t4 + e.
+template <int KIND, int D, int NQ>
+SD_DEVINL void ca_scores(const Rows<KIND, D>& rw, const Queries<D, NQ>& q, int lane, float (&s)[NQ][4]) {
     constexpr bool F16 = KIND != kBf16;
-    float s[NQ][4];
 #pragma unroll
     for (int nq = 0; nq < NQ; ++nq)
 #pragma unroll
@@ -208,84 +237,114 @@ SD_DEVINL void ca_step(const Rows<KIND, D>& rw, const uint32_t (&qf)[D / 16][NQ]
                 const uint32_t a0 = widen<KIND>(x0, false), a2 = widen<KIND>(x0, true);
                 const uint32_t a1 = widen<KIND>(x1, false), a3 = widen<KIND>(x1, true);
 #pragma unroll
-                for (int nq = 0; nq < NQ; ++nq)
-                    mma16<F16>(s[nq], a0, a1, a2, a3, qf[4 * c + kk][nq][0], qf[4 * c + kk][nq][1]);
+                for (int nq = 0; nq < NQ; ++nq) {
+                    const uint2 b = q.at(4 * c + kk, nq, lane);
+                    mma16<F16>(s[nq], a0, a1, a2, a3, b.x, b.y);
+                }
             }
         } else {
 #pragma unroll
             for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
-                for (int nq = 0; nq < NQ; ++nq)
-                    mma16<F16>(s[nq], w0[2 * kk], w1[2 * kk], w0[2 * kk + 1], w1[2 * kk + 1], qf[2 * c + kk][nq][0],
-                               qf[2 * c + kk][nq][1]);
+                for (int nq = 0; nq < NQ; ++nq) {
+                    const uint2 b = q.at(2 * c + kk, nq, lane);
+                    mma16<F16>(s[nq], w0[2 * kk], w1[2 * kk], w0[2 * kk + 1], w1[2 * kk + 1], b.x, b.y);
+                }
         }
     }
-    float ks[2] = {1.f, 1.f}, ev[2] = {0.f, 0.f}, mant[2] = {1.f, 1.f};
-    if constexpr (F16) {
+}
+
+// The online softmax of a step: s becomes the weights of the V rows.  MASK: rows above a query's
+// limit (sl[8nq + 2t4 + e]) take no part (pos: the positions of rows g8, g8 + 8).
+template <int KIND, int D, int NQ, bool MASK>
+SD_DEVINL void ca_softmax(float (&s)[NQ][4], const float (&ks)[2], const float (&vs)[2], const int (&pos)[2],
+                          const int* sl, int t4, const Queries<D, NQ>& q, CaState<D, NQ>& st) {
+    constexpr bool F16 = KIND != kBf16;
+    float top = -INFINITY, wide = 0.f;
+    float w[NQ][4];
+    auto weights = [&]() {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            ks[h] = KIND == kE4m3 ? rw.ks[h] * 256.f : rw.ks[h];
-            const uint32_t b = __float_as_uint(rw.vs[h]);
-            const uint32_t e = (b >> 23) & 0xffu;
-            ev[h] = (float)((int)e - 127);
-            mant[h] = e == 0u ? 0.f : __uint_as_float((b & 0x7fffffu) | 0x3f800000u);  // scale = mant * 2^ev
+        for (int nq = 0; nq < NQ; ++nq)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int e = i & 1, h = i >> 1;
+                const float dx = s[nq][i] - st.m[nq][e];
+                top = fmaxf(top, dx);
+                const float p = fast_exp2(dx);
+                w[nq][i] = p;
+                if constexpr (F16) wide = fmaxf(wide, p * vs[h] * st.c[nq][e]);
+            }
+    };
+#pragma unroll
+    for (int nq = 0; nq < NQ; ++nq)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int e = i & 1, h = i >> 1;
+            const float x = s[nq][i] * (F16 ? ks[h] * q.qs[nq][e] : q.qs[nq][e]);
+            s[nq][i] = MASK && pos[h] > sl[8 * nq + 2 * t4 + e] ? -INFINITY : x;
         }
-    }
-    uint32_t ph[NQ][2], pl[NQ][2];
+    weights();
+    if (__any_sync(0xffffffffu, top > kGrow || wide > kLimF16)) {
 #pragma unroll
-    for (int nq = 0; nq < NQ; ++nq) {
-        float w[4];
+        for (int nq = 0; nq < NQ; ++nq)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            float x[2];
-            bool on[2];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                on[h] = rw.pos[h] <= lim[nq][e];
-                const float f = F16 ? ks[h] * qs[nq][e] : qs[nq][e];
-                x[h] = on[h] ? s[nq][2 * h + e] * f : -INFINITY;
-            }
-            const float mo = st.m[nq][e];
-            const float mn = fmaxf(mo, max_over_rows(fmaxf(x[0], x[1])));
-            const float ref = mn == -INFINITY ? 0.f : mn;
-            const float p0 = fast_exp2(x[0] - ref), p1 = fast_exp2(x[1] - ref);
-            float alpha = fast_exp2(mo - ref);
-            st.m[nq][e] = mn;
-            st.l[nq][e] = st.l[nq][e] * alpha + (p0 + p1);
-            if constexpr (F16) {
-                const float y0 = on[0] ? x[0] + ev[0] : -INFINITY, y1 = on[1] ? x[1] + ev[1] : -INFINITY;
-                const float m2o = st.m2[nq][e];
-                const float m2n = fmaxf(m2o, max_over_rows(fmaxf(y0, y1)));
-                const float r2 = m2n == -INFINITY ? 0.f : m2n;
-                alpha = fast_exp2(m2o - r2);
-                st.m2[nq][e] = m2n;
-                w[e] = on[0] ? fast_exp2(y0 - r2 + 14.f) * mant[0] : 0.f;
-                w[2 + e] = on[1] ? fast_exp2(y1 - r2 + 14.f) * mant[1] : 0.f;
-            } else {
-                w[e] = p0;
-                w[2 + e] = p1;
-            }
-            if (alpha != 1.f) {
+            for (int e = 0; e < 2; ++e) {
+                const float mo = st.m[nq][e];
+                const float mn = fmaxf(mo, max_over_rows(fmaxf(s[nq][e], s[nq][2 + e])));
+                const float fl = fast_exp2(mo - mn);
+                float fo = fl;
+                if constexpr (F16) {
+                    // log2 of a zero scale is -inf: its row asks for nothing.  The product's maximum is never so
+                    // far below m that c would overflow
+                    float y = fmaxf(s[nq][e] + __log2f(vs[0]), s[nq][2 + e] + __log2f(vs[1]));
+                    y = max_over_rows(y);
+                    const float co = st.c[nq][e];
+                    const float m2o = co > 0.f ? mo + kTopF16 - __log2f(co) : kNone;
+                    const float m2n = fmaxf(fmaxf(m2o, y), mn - 100.f);
+                    if (mn > kNone) {
+                        st.c[nq][e] = fast_exp2(mn - m2n + kTopF16);
+                        fo = co > 0.f ? fl * st.c[nq][e] / co : 0.f;
+                    }
+                }
+                st.m[nq][e] = mn;
+                st.l[nq][e] *= fl;
 #pragma unroll
                 for (int md = 0; md < D / 16; ++md) {
-                    st.o[md][nq][e] *= alpha;
-                    st.o[md][nq][2 + e] *= alpha;
+                    st.o[md][nq][e] *= fo;
+                    st.o[md][nq][2 + e] *= fo;
                 }
             }
+        weights();
+    }
+#pragma unroll
+    for (int nq = 0; nq < NQ; ++nq)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int e = i & 1, h = i >> 1;
+            st.l[nq][e] += w[nq][i];
+            s[nq][i] = F16 ? w[nq][i] * vs[h] * st.c[nq][e] : w[nq][i];
         }
-        // P^T (rows by lane group) to the B operand (rows by lane pair)
+}
+
+// O^T += V^T P^T of a step, P in s.
+template <int KIND, int D, int NQ, bool HILO>
+SD_DEVINL void ca_output(const Rows<KIND, D>& rw, const float (&s)[NQ][4], CaState<D, NQ>& st) {
+    constexpr bool F16 = KIND != kBf16;
+    uint32_t ph[NQ][2], pl[NQ][2];
+#pragma unroll
+    for (int nq = 0; nq < NQ; ++nq)  // P^T (rows by lane group) to the B operand (rows by lane pair)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            uint32_t lo;
-            ph[nq][h] = movmatrix_t(weight_word<F16>(w[2 * h], w[2 * h + 1], HILO ? &lo : nullptr));
+            uint32_t hi, lo = 0u;
+            weight_words<F16, HILO>(s[nq][2 * h], s[nq][2 * h + 1], hi, lo);
+            ph[nq][h] = movmatrix_t(hi);
             if constexpr (HILO) pl[nq][h] = movmatrix_t(lo);
         }
-    }
     auto pv = [&](int md, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
 #pragma unroll
         for (int nq = 0; nq < NQ; ++nq) {
-            mma16<F16>(st.o[md][nq], a0, a1, a2, a3, ph[nq][0], ph[nq][1]);
             if constexpr (HILO) mma16<F16>(st.o[md][nq], a0, a1, a2, a3, pl[nq][0], pl[nq][1]);
+            mma16<F16>(st.o[md][nq], a0, a1, a2, a3, ph[nq][0], ph[nq][1]);
         }
     };
 #pragma unroll
@@ -312,7 +371,18 @@ SD_DEVINL int seq_len(const CaParams& p, int b) {
     for (int v = 0; v < p.V; ++v) m = max(m, p.qpos[(size_t)b * p.V + v]);
     return min(m, p.T - 1) + 1;
 }
-SD_DEVINL int tiles_of(int rows) { return max(1, (rows + kCaTile - 1) / kCaTile); }
+SD_DEVINL unsigned tiles_of(int rows) { return (unsigned)max(1, (rows + kCaTile - 1) / kCaTile); }
+
+// W units cut into n runs (n <= W): the first W % n have one more.  The run that holds unit x.
+struct Cut {
+    unsigned q, rem;
+    SD_DEVINL Cut(unsigned W, unsigned n) : q(W / n), rem(W % n) {}
+    SD_DEVINL unsigned start(unsigned c) const { return c * q + min(c, rem); }
+    SD_DEVINL unsigned run_of(unsigned x) const {
+        const unsigned big = rem * (q + 1);
+        return x < big ? x / (q + 1) : rem + (x - big) / q;
+    }
+};
 
 SD_DEVINL void store_pair(void* out, bool bf16, size_t i, float x, float y) {  // elements i, i + 1 (i even)
     if (bf16)
@@ -321,103 +391,114 @@ SD_DEVINL void store_pair(void* out, bool bf16, size_t i, float x, float y) {  /
         reinterpret_cast<float2*>(out)[i / 2] = make_float2(x, y);
 }
 
+template <int D, int NQ>
+struct CaShared {
+    // a state row: column g8 * D/8 + 2md + j at 18 md + 2 g8 + j
+    static constexpr int kPitch = D / 16 * 18;
+    float o[kCaWarps][8 * NQ][kPitch];
+    float2 ml[kCaWarps][8 * NQ];
+    uint2 q[NQ >= 2 ? D / 16 * NQ * 32 : 1];
+    int lim[8 * NQ];
+    unsigned part[kCaWarps], base;
+    int b;
+};
+
+constexpr int kFoldSteps = 32;  // steps after which SD_F32 output folds the accumulators
+
 template <int KIND, int D, int NQ, bool HILO, bool SEL, int MINB>
 __global__ void __launch_bounds__(kCaThreads, MINB) cache_attend_kernel(const CaParams p) {
     constexpr bool F16 = KIND != kBf16;
-    constexpr int kEs = Rows<KIND, D>::kEs;
+    constexpr int kRow = Rows<KIND, D>::kRow;
     constexpr int kMd = D / 16;
-    constexpr int kPitch = kMd * 18;  // a state row in shared memory: column g8*D/8 + 2md + j at 18 md + 2 g8 + j
-    __shared__ float so[kCaWarps][8 * NQ][kPitch];
-    __shared__ float2 sml[kCaWarps][8 * NQ];
-    __shared__ int s_part[kCaWarps], s_b, s_base;
+    extern __shared__ uint4 ca_smem[];
+    auto& sh = *reinterpret_cast<CaShared<D, NQ>*>(ca_smem);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g8 = lane >> 2, t4 = lane & 3;
-    const int c = (int)blockIdx.x;
+    const unsigned c = blockIdx.x;
     pdl_wait();  // the cache, qpos and q may be the preceding kernels' results
     pdl_launch_dependents();
 
-    // this CTA's run of units: [w0, w1) of all groups' units in order; no CTA of the ncta that
-    // take part has an empty run, so a group's runs are in consecutive slots
-    long W;
-    int ncta;
-    int b, kvh, j, tb;
-    long w0, w1;
+    // this CTA's run of units: [w0, w1) of all groups' units in order; no run is empty, so a
+    // group's runs are in consecutive slots
+    unsigned W, tb, j, w0;
+    int b, kvh;
     if constexpr (SEL) {
         tb = tiles_of(p.n_list);
-        W = (long)p.B * p.Hkv * tb;
-        ncta = (int)min((long)gridDim.x, W);
-        if (c >= ncta) return;
-        w0 = c * W / ncta;
-        w1 = (c + 1) * W / ncta;
-        const int g = (int)(w0 / tb);
-        j = (int)(w0 - (long)g * tb);
-        b = g / p.Hkv;
-        kvh = g - b * p.Hkv;
+        W = (unsigned)p.B * p.Hkv * tb;
     } else {
-        int sum = 0;
+        unsigned sum = 0;
         for (int i = tid; i < p.B; i += kCaThreads) sum += tiles_of(seq_len(p, i));
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        if (lane == 0) s_part[warp] = sum;
+        if (lane == 0) sh.part[warp] = sum;
         __syncthreads();
-        W = ((long)s_part[0] + s_part[1] + s_part[2] + s_part[3]) * p.Hkv;
-        ncta = (int)min((long)gridDim.x, W);
-        if (c >= ncta) return;
-        w0 = c * W / ncta;
-        w1 = (c + 1) * W / ncta;
+        W = (sh.part[0] + sh.part[1] + sh.part[2] + sh.part[3]) * p.Hkv;
+    }
+    const unsigned ncta = min(gridDim.x, W);
+    if (c >= ncta) return;
+    const Cut cut(W, ncta);
+    w0 = cut.start(c);
+    const unsigned w1 = cut.start(c + 1);
+    if constexpr (SEL) {
+        const unsigned g = w0 / tb;
+        j = w0 - g * tb;
+        b = (int)(g / (unsigned)p.Hkv);
+        kvh = (int)(g - (unsigned)b * p.Hkv);
+    } else {
         // the sequence of unit w0: sequence i's units start at Hkv * (tiles before it)
-        int run = 0;
+        unsigned run = 0;
         for (int base = 0; base < p.B; base += kCaThreads) {
             const int i = base + tid;
-            const int t = i < p.B ? tiles_of(seq_len(p, i)) : 0;
-            int incl = t;
+            const unsigned t = i < p.B ? tiles_of(seq_len(p, i)) : 0u;
+            unsigned incl = t;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const int u = __shfl_up_sync(0xffffffffu, incl, o);
+                const unsigned u = __shfl_up_sync(0xffffffffu, incl, o);
                 if (lane >= o) incl += u;
             }
             __syncthreads();
-            if (lane == 31) s_part[warp] = incl;
-            if (tid == 0) s_b = -1;
+            if (lane == 31) sh.part[warp] = incl;
+            if (tid == 0) sh.b = -1;
             __syncthreads();
-            int before = run;
-            for (int k = 0; k < warp; ++k) before += s_part[k];
-            const long hi = (long)(before + incl) * p.Hkv, lo = hi - (long)t * p.Hkv;
-            if (t > 0 && w0 >= lo && w0 < hi) {
-                s_b = i;
-                s_base = before + incl - t;
+            unsigned before = run;
+            for (int k = 0; k < warp; ++k) before += sh.part[k];
+            const unsigned hi = (before + incl) * p.Hkv, lo = hi - t * p.Hkv;
+            if (t > 0u && w0 >= lo && w0 < hi) {
+                sh.b = i;
+                sh.base = lo;
             }
-            for (int k = 0; k < kCaWarps; ++k) run += s_part[k];
+            for (int k = 0; k < kCaWarps; ++k) run += sh.part[k];
             __syncthreads();
-            if (s_b >= 0) break;
+            if (sh.b >= 0) break;
         }
-        b = s_b;
+        b = sh.b;
         tb = tiles_of(seq_len(p, b));
-        const int off = (int)(w0 - (long)s_base * p.Hkv);
-        kvh = off / tb;
-        j = off - kvh * tb;
+        const unsigned off = w0 - sh.base;
+        kvh = (int)(off / tb);
+        j = off - (unsigned)kvh * tb;
     }
 
-    const int halves = p.R > 8 * NQ ? 2 : 1;  // warps 0, 1 and 2, 3 take the query rows' halves (R > 16)
-    const int wh = kCaWarps / halves, half = warp / wh, w_in = warp - half * wh;
-    for (long w = w0; w < w1;) {
+    for (unsigned w = w0; w < w1;) {
         const int g = b * p.Hkv + kvh;
         const int len = seq_len(p, b);
-        const int seg = (int)min((long)(tb - j), w1 - w);
+        const unsigned seg = min(tb - j, w1 - w);
         const int list = SEL ? p.n_list : len;
-        const int j0 = j * kCaTile, j1 = len == 0 ? j0 : min(list, j0 + seg * kCaTile);
+        const int j0 = (int)j * kCaTile, j1 = len == 0 ? j0 : min(list, j0 + (int)seg * kCaTile);
 
-        // the query rows: 8nq + g8 of this half as B fragments
-        uint32_t qf[kMd][NQ][2];
-        float qs[NQ][2];
-        int lim[NQ][2];
+        // the query rows 8nq + g8 as B fragments, their limits and the smallest limit
+        Queries<D, NQ> q;
+        q.sh = sh.q;
+        __syncthreads();  // (the segment before is done with the limits and the states)
+        int lmin = p.T;  // rows every query sees
+        if (tid < 8 * NQ) sh.lim[tid] = tid < p.R ? min(p.qpos[(size_t)b * p.V + tid / p.G], p.T - 1) : -1;
+        for (int v = 0; v < p.V; ++v) lmin = min(lmin, p.qpos[(size_t)b * p.V + v] + 1);
 #pragma unroll
         for (int nq = 0; nq < NQ; ++nq) {
-            const int r = half * 8 * NQ + 8 * nq + g8;
+            const int r = 8 * nq + g8;
             const bool have = r < p.R;
             const int v = have ? r / p.G : 0, gi = have ? r - v * p.G : 0;
             const uint8_t* qrow = p.q + (((size_t)b * p.V + v) * p.Hq + (size_t)kvh * p.G + gi) * (D * 2);
+            uint32_t raw[kMd][2];
             if constexpr (F16) {
-                uint32_t raw[kMd][2];
                 uint32_t top = 0u;
 #pragma unroll
                 for (int cc = 0; cc < Rows<KIND, D>::kKc; ++cc)
@@ -441,39 +522,46 @@ __global__ void __launch_bounds__(kCaThreads, MINB) cache_attend_kernel(const Ca
                 for (int k = 0; k < kMd; ++k)
 #pragma unroll
                     for (int i = 0; i < 2; ++i)
-                        qf[k][nq][i] = pack_f16x2(bf16lo(raw[k][i]) * down, bf16hi(raw[k][i]) * down);
+                        raw[k][i] = pack_f16x2(bf16lo(raw[k][i]) * down, bf16hi(raw[k][i]) * down);
 #pragma unroll
                 for (int e2 = 0; e2 < 2; ++e2)
-                    qs[nq][e2] = __shfl_sync(0xffffffffu, up * p.scale_log2, (2 * t4 + e2) * 4);
+                    q.qs[nq][e2] = __shfl_sync(0xffffffffu, up * p.scale_log2, (2 * t4 + e2) * 4);
             } else {
 #pragma unroll
                 for (int cc = 0; cc < Rows<KIND, D>::kKc; ++cc) {  // dims 32 cc + 8 t4 ..
                     const uint4 x = have ? ld_row16(qrow + 2 * (32 * cc + 8 * t4)) : make_uint4(0u, 0u, 0u, 0u);
-                    qf[2 * cc][nq][0] = x.x;
-                    qf[2 * cc][nq][1] = x.y;
-                    qf[2 * cc + 1][nq][0] = x.z;
-                    qf[2 * cc + 1][nq][1] = x.w;
+                    raw[2 * cc][0] = x.x;
+                    raw[2 * cc][1] = x.y;
+                    raw[2 * cc + 1][0] = x.z;
+                    raw[2 * cc + 1][1] = x.w;
                 }
-                qs[nq][0] = qs[nq][1] = p.scale_log2;
+                q.qs[nq][0] = q.qs[nq][1] = p.scale_log2;
             }
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int rr = half * 8 * NQ + 8 * nq + 2 * t4 + e;
-                lim[nq][e] = rr < p.R ? min(p.qpos[(size_t)b * p.V + rr / p.G], p.T - 1) : -1;
+            for (int k = 0; k < kMd; ++k) {
+                if constexpr (Queries<D, NQ>::kShared) {
+                    if (warp == nq) sh.q[(k * NQ + nq) * 32 + lane] = make_uint2(raw[k][0], raw[k][1]);
+                } else {
+                    q.f[k][nq][0] = raw[k][0];
+                    q.f[k][nq][1] = raw[k][1];
+                }
             }
         }
+        __syncthreads();
 
         CaState<D, NQ> st;
         st.init();
-        const uint8_t* kbase = p.kc + (size_t)g * p.T * (D * kEs);
-        const uint8_t* vbase = p.vc + (size_t)g * p.T * (D * kEs);
-        // lane l < 16 resolves list row l of a step (SEL): its position, or -1 (an empty slot, an
-        // index outside the cache, a row no query sees)
+        const uint8_t* kbase = p.kc + (size_t)g * p.T * kRow;
+        const uint8_t* vbase = p.vc + (size_t)g * p.T * kRow;
+        const float* ksb = p.ks + (size_t)g * p.T;
+        const float* vsb = p.vs + (size_t)g * p.T;
+        // lane l < 16 (and l + 16) resolves list row l of a step (SEL): its position, or -1 (an empty
+        // slot, an index outside the cache, a row no query sees)
         auto resolve = [&](int step) {
             int t = -1;
             const int i = j0 + 16 * step + (lane & 15);
             if (i < j1) {
-                const int e = i / p.block;
+                const int e = (int)((unsigned)i / (unsigned)p.block);
                 const long sel = p.idx[(size_t)g * p.n_idx + e];
                 const long pos = sel * p.block + (i - e * p.block);
                 if (sel != -1) {
@@ -485,90 +573,160 @@ __global__ void __launch_bounds__(kCaThreads, MINB) cache_attend_kernel(const Ca
             }
             return t;
         };
-        auto fetch = [&](int step, int mine, Rows<KIND, D>& rw) {
-            const int i0 = j0 + 16 * step;
-            // list row i of the step as a position to read (always one that a query sees)
-            auto at = [&](int i, int* pos) {
-                if constexpr (SEL) {
-                    const int t = __shfl_sync(0xffffffffu, mine, i);
-                    if (pos != nullptr) *pos = t < 0 ? 0x7fffffff : t;
-                    return max(t, 0);
-                } else {
-                    if (pos != nullptr) *pos = i0 + i;  // at or past len: above every limit
-                    return min(i0 + i, len - 1);
-                }
-            };
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int t = at(g8 + 8 * h, &rw.pos[h]);
-                rw.load_k(h, kbase + (size_t)t * (D * kEs), t4);
+        // row i of a step as a position to read: always one that a query sees
+        auto row_at = [&](int step, int rows, int i) {
+            if constexpr (SEL) return max(__shfl_sync(0xffffffffu, rows, i), 0);
+            return min(j0 + 16 * step + i, len - 1);
+        };
+        Rows<KIND, D> rw;
+        auto fetch_k = [&](int step, int rows) {
+            if (!SEL && j0 + 16 * step + 16 <= len) {
+                const int t = j0 + 16 * step + g8;
+                const uint8_t* kp = kbase + (size_t)t * kRow + 16 * t4;
+                rw.load_k(0, kp);
+                rw.load_k(1, kp + 8 * kRow);
                 if constexpr (F16) {
-                    rw.ks[h] = __ldg(p.ks + (size_t)g * p.T + t);
-                    rw.vs[h] = __ldg(p.vs + (size_t)g * p.T + t);
+                    rw.ks[0] = __ldg(ksb + t), rw.ks[1] = __ldg(ksb + t + 8);
+                    rw.vs[0] = __ldg(vsb + t), rw.vs[1] = __ldg(vsb + t + 8);
                 }
-            }
+            } else {
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int t = at(2 * t4 + (r & 1) + 8 * (r >> 1), nullptr);
-                rw.load_v(r, vbase + (size_t)t * (D * kEs), g8);
+                for (int h = 0; h < 2; ++h) {
+                    const int t = row_at(step, rows, g8 + 8 * h);
+                    rw.load_k(h, kbase + (size_t)t * kRow + 16 * t4);
+                    if constexpr (F16) {
+                        rw.ks[h] = __ldg(ksb + t);
+                        rw.vs[h] = __ldg(vsb + t);
+                    }
+                }
             }
         };
-        const int nsteps = (j1 - j0 + 15) / 16;
-        if (w_in < nsteps) {
-            Rows<KIND, D> cur, nxt;
-            int mine = -1;
-            if constexpr (SEL) mine = resolve(w_in);
-            fetch(w_in, mine, nxt);
-            if constexpr (SEL) mine = resolve(w_in + wh);
-            for (int s = w_in; s < nsteps; s += wh) {
-                cur = nxt;
-                if (s + wh < nsteps) {
-                    fetch(s + wh, mine, nxt);
-                    if constexpr (SEL) mine = resolve(s + 2 * wh);
+        auto fetch_v = [&](int step, int rows) {
+            if (!SEL && j0 + 16 * step + 16 <= len) {
+                const uint8_t* vp = vbase + (size_t)(j0 + 16 * step + 2 * t4) * kRow + g8 * (kRow / 8);
+                rw.load_v(0, vp);
+                rw.load_v(1, vp + kRow);
+                rw.load_v(2, vp + 8 * kRow);
+                rw.load_v(3, vp + 9 * kRow);
+            } else {
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int t = row_at(step, rows, 2 * t4 + (r & 1) + 8 * (r >> 1));
+                    rw.load_v(r, vbase + (size_t)t * kRow + g8 * (kRow / 8));
                 }
-                ca_step<KIND, D, NQ, HILO>(cur, qf, qs, lim, st);
+            }
+        };
+        // Folds the registers' state into the warp's in shared memory (all of it relative to the softmax
+        // maximum m), and starts it anew.
+        auto fold = [&](bool first) {
+#pragma unroll
+            for (int nq = 0; nq < NQ; ++nq)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int qr = 8 * nq + 2 * t4 + e;
+                    const float l = sum_over_rows(st.l[nq][e]);
+                    float f = 1.f;
+                    if constexpr (F16) f = st.c[nq][e] > 0.f ? 1.f / st.c[nq][e] : 0.f;
+                    float2 ml = make_float2(st.m[nq][e], l);
+                    float old = 0.f;
+                    if (!first) {
+                        const float2 was = sh.ml[warp][qr];
+                        ml.x = fmaxf(was.x, st.m[nq][e]);
+                        old = exp2f(was.x - ml.x);
+                        const float now = exp2f(st.m[nq][e] - ml.x);
+                        f *= now;
+                        ml.y = was.y * old + l * now;
+                    }
+                    float* row = sh.o[warp][qr];
+#pragma unroll
+                    for (int md = 0; md < kMd; ++md) {
+                        float2* at = reinterpret_cast<float2*>(row + 18 * md + 2 * g8);
+                        float2 x = make_float2(st.o[md][nq][e] * f, st.o[md][nq][2 + e] * f);
+                        if (!first) {
+                            const float2 y = *at;
+                            x.x = fmaf(y.x, old, x.x);
+                            x.y = fmaf(y.y, old, x.y);
+                        }
+                        *at = x;
+                    }
+                    __syncwarp();
+                    if (g8 == 0) sh.ml[warp][qr] = ml;
+                }
+            __syncwarp();
+            st.clear();
+        };
+
+        const int nsteps = (j1 - j0 + 15) / 16;
+        bool first = true;
+        if (warp < nsteps) {
+            int rows = -1, next = -1;
+            if constexpr (SEL) {
+                rows = resolve(warp);
+                next = resolve(warp + kCaWarps);
+            }
+            fetch_k(warp, rows);
+            fetch_v(warp, rows);
+            int since = 0;
+            for (int s = warp; s < nsteps; s += kCaWarps) {
+                const bool more = s + kCaWarps < nsteps;
+                float sc[NQ][4];
+                ca_scores<KIND, D, NQ>(rw, q, lane, sc);
+                int pos[2];
+                if constexpr (SEL) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int t = __shfl_sync(0xffffffffu, rows, g8 + 8 * h);
+                        pos[h] = t < 0 ? 0x7fffffff : t;
+                    }
+                } else {
+                    pos[0] = j0 + 16 * s + g8;
+                    pos[1] = pos[0] + 8;
+                }
+                const float ks[2] = {rw.ks[0], rw.ks[1]}, vs[2] = {rw.vs[0], rw.vs[1]};
+                if (more) fetch_k(s + kCaWarps, next);
+                bool all = true;
+                if constexpr (SEL)
+                    all = __all_sync(0xffffffffu, max(pos[0], pos[1]) < lmin);
+                else
+                    all = j0 + 16 * s + 16 <= lmin;
+                if (all)
+                    ca_softmax<KIND, D, NQ, false>(sc, ks, vs, pos, sh.lim, t4, q, st);
+                else
+                    ca_softmax<KIND, D, NQ, true>(sc, ks, vs, pos, sh.lim, t4, q, st);
+                ca_output<KIND, D, NQ, HILO>(rw, sc, st);
+                if (more) fetch_v(s + kCaWarps, next);
+                if constexpr (SEL) {
+                    rows = next;
+                    next = resolve(s + 2 * kCaWarps);
+                }
+                if (HILO && ++since == kFoldSteps) {
+                    fold(first);
+                    first = false;
+                    since = 0;
+                }
             }
         }
-
-        // the warps' states to shared memory, all relative to the softmax maximum m
-#pragma unroll
-        for (int nq = 0; nq < NQ; ++nq)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                float l = st.l[nq][e];
-                l += __shfl_xor_sync(0xffffffffu, l, 4);
-                l += __shfl_xor_sync(0xffffffffu, l, 8);
-                l += __shfl_xor_sync(0xffffffffu, l, 16);
-                const int q = 8 * nq + 2 * t4 + e;
-                float f = 1.f;
-                if constexpr (F16)
-                    f = st.m2[nq][e] == -INFINITY ? 0.f
-                                                  : exp2f(st.m2[nq][e] - st.m[nq][e] - (KIND == kE4m3 ? 6.f : 14.f));
-#pragma unroll
-                for (int md = 0; md < kMd; ++md) {
-                    so[warp][q][18 * md + 2 * g8] = st.o[md][nq][e] * f;
-                    so[warp][q][18 * md + 2 * g8 + 1] = st.o[md][nq][2 + e] * f;
-                }
-                if (g8 == 0) sml[warp][q] = make_float2(st.m[nq][e], l);
-            }
+        fold(first);
         __syncthreads();
-        const bool whole = j == 0 && seg == tb && p.P == 0;
+        const bool whole = j == 0u && seg == tb && p.P == 0;
         const size_t slot = (size_t)c + g;
         for (int i = tid; i < p.R * (D / 2); i += kCaThreads) {
             const int r = i / (D / 2), d = 2 * (i - r * (D / 2));
-            const int q = r % (8 * NQ), wb = r / (8 * NQ) * wh;
             const int gg = d / (D / 8), at = 18 * ((d - gg * (D / 8)) / 2) + 2 * gg;
-            float M = -INFINITY;
-            for (int k = 0; k < wh; ++k) M = fmaxf(M, sml[wb + k][q].x);
+            float M = sh.ml[0][r].x;
+#pragma unroll
+            for (int k = 1; k < kCaWarps; ++k) M = fmaxf(M, sh.ml[k][r].x);
             float L = 0.f, x = 0.f, y = 0.f;
-            if (M != -INFINITY)
-                for (int k = 0; k < wh; ++k) {
-                    const float2 ml = sml[wb + k][q];
-                    const float f = exp2f(ml.x - M);
-                    L = fmaf(ml.y, f, L);
-                    x = fmaf(so[wb + k][q][at], f, x);
-                    y = fmaf(so[wb + k][q][at + 1], f, y);
-                }
+#pragma unroll
+            for (int k = 0; k < kCaWarps; ++k) {
+                const float2 ml = sh.ml[k][r];
+                const float2 o = *reinterpret_cast<const float2*>(&sh.o[k][r][at]);
+                const float f = exp2f(ml.x - M);
+                L = fmaf(ml.y, f, L);
+                x = fmaf(o.x, f, x);
+                y = fmaf(o.y, f, y);
+            }
+            if (M == kNone) M = -INFINITY;
             if (whole) {
                 const int v = r / p.G;
                 const size_t row = ((size_t)b * p.V + v) * p.Hq + (size_t)kvh * p.G + (r - v * p.G);
@@ -580,12 +738,8 @@ __global__ void __launch_bounds__(kCaThreads, MINB) cache_attend_kernel(const Ca
                 if (d == 0) p.ws.ml[slot * p.R + r] = make_float2(M, L);
             }
         }
-        if (j == 0 && tid == 0) {
-            // the group's last unit w + tb - 1 is of CTA ((w + tb) * ncta - 1) / W
-            const int last = (int)(((w + tb) * ncta - 1) / W);
-            p.ws.meta[g] = make_int2(c + g, last - c + 1);
-        }
-        __syncthreads();
+        if (j == 0u && tid == 0)  // the runs that hold the group's units
+            p.ws.meta[g] = make_int2((int)c + g, (int)(cut.run_of(w + tb - 1) - c) + 1);
         w += seg;
         j = 0;
         if (++kvh == p.Hkv) {
@@ -596,22 +750,22 @@ __global__ void __launch_bounds__(kCaThreads, MINB) cache_attend_kernel(const Ca
     }
 }
 
-// One warp a query row: the states of its group's runs and of the prefix's splits into the output.
+// One CTA a query row: the states of its group's runs and of the prefix's splits into the output.
+// Each warp takes every fourth state; a row's states are loaded together, and the warps' sums
+// meet in shared memory in a fixed order.
 template <int D>
 __global__ void __launch_bounds__(kCaThreads) cache_merge_kernel(const CaParams p) {
+    __shared__ float so[kCaWarps][D];
+    __shared__ float sl[kCaWarps], sm[kCaWarps];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int h = (int)blockIdx.x, v = (int)blockIdx.y, b = (int)blockIdx.z;
+    const int kvh = h / p.G, gi = h - kvh * p.G, r = v * p.G + gi;
+    const unsigned M = (unsigned)p.B * p.R, mrow = ((unsigned)b * p.V + v) * p.G + gi;
     pdl_wait();
     pdl_launch_dependents();
-    const int lane = threadIdx.x & 31;
-    const long row = (long)blockIdx.x * kCaWarps + (threadIdx.x >> 5);  // (b, v, h)
-    if (row >= (long)p.B * p.V * p.Hq) return;
-    const int h = (int)(row % p.Hq);
-    const long bv = row / p.Hq;
-    const int b = (int)(bv / p.V), v = (int)(bv - (long)b * p.V);
-    const int kvh = h / p.G, gi = h - kvh * p.G, r = v * p.G + gi;
-    const int2 own = p.ws.meta[(size_t)b * p.Hkv + kvh];
+    const int2 own = p.ws.meta[b * p.Hkv + kvh];
     const int n = own.y + p.pre_splits;
     if (own.y == 1 && p.P == 0) return;  // written by the CTA that had the whole group
-    const size_t M = (size_t)p.B * p.R, mrow = (size_t)bv * p.G + gi;
     auto ml_of = [&](int i) {
         return i < own.y ? p.ws.ml[(size_t)(own.x + i) * p.R + r]
                          : p.ws.pre_ml[((size_t)kvh * p.pre_splits + (i - own.y)) * M + mrow];
@@ -620,47 +774,77 @@ __global__ void __launch_bounds__(kCaThreads) cache_merge_kernel(const CaParams 
         return i < own.y ? p.ws.o + ((size_t)(own.x + i) * p.R + r) * D
                          : p.ws.pre_o + (((size_t)kvh * p.pre_splits + (i - own.y)) * M + mrow) * D;
     };
-    float mx = -INFINITY;
-    for (int i = lane; i < n; i += 32) mx = fmaxf(mx, ml_of(i).x);
-    mx = warp_max(mx);
-    const float ref = mx == -INFINITY ? 0.f : mx;
     constexpr int kE = D / 32;  // columns a lane holds
-    float acc[kE] = {}, L = 0.f;
-    for (int base = 0; base < n; base += 32) {
-        float2 ml = make_float2(-INFINITY, 0.f);
-        if (base + lane < n) ml = ml_of(base + lane);
-        const float f = exp2f(ml.x - ref);  // 0 for a state without rows
-        L = fmaf(ml.y, f, L);
-        const int cnt = min(32, n - base);
-#pragma unroll 8
-        for (int k = 0; k < cnt; ++k) {
-            const float fk = __shfl_sync(0xffffffffu, f, k);
-            const float* o = o_of(base + k) + kE * lane;
-            if constexpr (kE == 4) {
-                const float4 x = *reinterpret_cast<const float4*>(o);
-                acc[0] = fmaf(x.x, fk, acc[0]);
-                acc[1] = fmaf(x.y, fk, acc[1]);
-                acc[2] = fmaf(x.z, fk, acc[2]);
-                acc[3] = fmaf(x.w, fk, acc[3]);
-            } else {
-                const float2 x = *reinterpret_cast<const float2*>(o);
-                acc[0] = fmaf(x.x, fk, acc[0]);
-                acc[1] = fmaf(x.y, fk, acc[1]);
+    float acc[kE] = {}, L = 0.f, top = kNone;
+    for (int base = warp; base < n; base += 32 * kCaWarps) {  // states base + 4k
+        const int mine = base + kCaWarps * lane;
+        float2 ml = make_float2(kNone, 0.f);
+        if (mine < n) ml = ml_of(mine);
+        const float was = top;
+        top = fmaxf(top, warp_max(ml.x));
+        const float f = exp2f(fmaxf(ml.x, kNone) - top), fo = exp2f(was - top);
+        L = L * fo + ml.y * f;
+#pragma unroll
+        for (int e = 0; e < kE; ++e) acc[e] *= fo;
+        const int cnt = min(32, (n - base + kCaWarps - 1) / kCaWarps);
+        for (int k0 = 0; k0 < cnt; k0 += 8) {
+            float x[8][kE];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const float* o = o_of(base + kCaWarps * min(k0 + k, cnt - 1)) + kE * lane;
+                if constexpr (kE == 4) {
+                    const float4 y = *reinterpret_cast<const float4*>(o);
+                    x[k][0] = y.x, x[k][1] = y.y, x[k][2] = y.z, x[k][3] = y.w;
+                } else {
+                    const float2 y = *reinterpret_cast<const float2*>(o);
+                    x[k][0] = y.x, x[k][1] = y.y;
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const float fk = __shfl_sync(0xffffffffu, f, min(k0 + k, 31));
+                if (k0 + k < cnt) {
+#pragma unroll
+                    for (int e = 0; e < kE; ++e) acc[e] = fmaf(x[k][e], fk, acc[e]);
+                }
             }
         }
     }
     L = warp_sum(L);
-    const float inv = L > 0.f ? 1.f / L : 0.f;
 #pragma unroll
-    for (int e = 0; e < kE; e += 2)
-        store_pair(p.out, p.out_bf16 != 0, (size_t)row * D + kE * lane + e, acc[e] * inv, acc[e + 1] * inv);
-    if (lane == 0) p.lse[row] = L > 0.f ? (mx + log2f(L)) * 0.69314718055994530942f : -INFINITY;
+    for (int e = 0; e < kE; ++e) so[warp][kE * lane + e] = acc[e];
+    if (lane == 0) {
+        sl[warp] = L;
+        sm[warp] = top;
+    }
+    __syncthreads();
+    float mx = sm[0], f[kCaWarps];
+#pragma unroll
+    for (int k = 1; k < kCaWarps; ++k) mx = fmaxf(mx, sm[k]);
+    L = 0.f;
+#pragma unroll
+    for (int k = 0; k < kCaWarps; ++k) {
+        f[k] = exp2f(sm[k] - mx);
+        L = fmaf(sl[k], f[k], L);
+    }
+    const float inv = L > 0.f ? 1.f / L : 0.f;
+    const size_t row = ((size_t)b * p.V + v) * p.Hq + h;
+    if (threadIdx.x < D / 2) {
+        const int d = 2 * (int)threadIdx.x;
+        float x = 0.f, y = 0.f;
+#pragma unroll
+        for (int k = 0; k < kCaWarps; ++k) {
+            x = fmaf(so[k][d], f[k], x);
+            y = fmaf(so[k][d + 1], f[k], y);
+        }
+        store_pair(p.out, p.out_bf16 != 0, row * D + d, x * inv, y * inv);
+    }
+    if (threadIdx.x == 0) p.lse[row] = L > 0.f ? (mx + log2f(L)) * 0.69314718055994530942f : -INFINITY;
 }
 
-// CTAs an SM holds of a variant (its __launch_bounds__): what its registers allow without spills
-// (8-bit codes, d = 128: 168 and 240 registers a thread for one and two query tiles).
+// CTAs an SM holds of a variant (its __launch_bounds__): what its registers allow without spills.
 constexpr int ca_ctas_per_sm(int kind, int d, int nq) {
-    return kind == kBf16 ? (d == 64 && nq == 1 ? 3 : 2) : (d == 64 ? 5 : 4) - nq;
+    return nq == 4 ? (d == 64 ? 3 : 2) : (kind == kBf16 && d == 128) || nq == 2 ? 3 : 4;
 }
 
 int ca_kind(const sd_cache_attend_args* a) {
@@ -673,7 +857,7 @@ CaPlan ca_plan(const sd_cache_attend_args* a) {
     const int R = (a->Hq / a->Hkv) * a->V;
     const long rows = a->idx != nullptr ? (long)a->n_idx * a->block : a->T;
     const long units = NG * std::max<long>(1, (rows + kCaTile - 1) / kCaTile);
-    pl.ctas = (int)std::min<long>(units, (long)num_sms() * ca_ctas_per_sm(ca_kind(a), a->d, R <= 8 ? 1 : 2));
+    pl.ctas = (int)std::min<long>(units, (long)num_sms() * ca_ctas_per_sm(ca_kind(a), a->d, R <= 8 ? 1 : R <= 16 ? 2 : 4));
     pl.slots = (int)(pl.ctas + NG - 1);
     pl.pre_splits = a->P > 0 ? prefix_splits(a) : 0;
     return pl;
@@ -717,19 +901,26 @@ sd_status ca_validate(const sd_cache_attend_args* a, bool pointers) {
 template <int KIND, int D, int NQ, bool HILO>
 sd_status ca_launch(const CaParams& p, const CaPlan& pl, cudaStream_t st) {
     constexpr int kMinB = ca_ctas_per_sm(KIND, D, NQ);
-    const dim3 grid((unsigned)pl.ctas), block(kCaThreads);
-    cudaError_t e = p.idx != nullptr
-                        ? launch_pdl(cache_attend_kernel<KIND, D, NQ, HILO, true, kMinB>, grid, block, 0, st, p)
-                        : launch_pdl(cache_attend_kernel<KIND, D, NQ, HILO, false, kMinB>, grid, block, 0, st, p);
-    SD_CUDA_CHECK(e, "sd_cache_attend: launch");
+    constexpr int kBytes = (int)sizeof(CaShared<D, NQ>);
+    auto kern = p.idx != nullptr ? cache_attend_kernel<KIND, D, NQ, HILO, true, kMinB>
+                                 : cache_attend_kernel<KIND, D, NQ, HILO, false, kMinB>;
+    if (kBytes > 48 * 1024)
+        SD_CUDA_CHECK(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes),
+                      "sd_cache_attend: cudaFuncSetAttribute");
+    SD_CUDA_CHECK(launch_pdl(kern, dim3((unsigned)pl.ctas), dim3(kCaThreads), (size_t)kBytes, st, p),
+                  "sd_cache_attend: launch");
     return launch_status("sd_cache_attend");
 }
 
+template <int KIND, int D, bool HILO>
+sd_status ca_dispatch_rows(const CaParams& p, const CaPlan& pl, cudaStream_t st) {
+    return p.R <= 8    ? ca_launch<KIND, D, 1, HILO>(p, pl, st)
+           : p.R <= 16 ? ca_launch<KIND, D, 2, HILO>(p, pl, st)
+                       : ca_launch<KIND, D, 4, HILO>(p, pl, st);
+}
 template <int KIND, int D>
 sd_status ca_dispatch(const CaParams& p, const CaPlan& pl, cudaStream_t st) {
-    if (p.out_bf16)
-        return p.R <= 8 ? ca_launch<KIND, D, 1, false>(p, pl, st) : ca_launch<KIND, D, 2, false>(p, pl, st);
-    return p.R <= 8 ? ca_launch<KIND, D, 1, true>(p, pl, st) : ca_launch<KIND, D, 2, true>(p, pl, st);
+    return p.out_bf16 ? ca_dispatch_rows<KIND, D, false>(p, pl, st) : ca_dispatch_rows<KIND, D, true>(p, pl, st);
 }
 
 }  // namespace
@@ -792,8 +983,7 @@ extern "C" sd_status sd_cache_attend(const sd_cache_attend_args* a, void* stream
         default: st = d128 ? ca_dispatch<kBf16, 128>(p, pl, cs) : ca_dispatch<kBf16, 64>(p, pl, cs); break;
     }
     if (st != SD_OK) return st;
-    const long rows = (long)a->B * a->V * a->Hq;
-    const dim3 grid((unsigned)((rows + kCaWarps - 1) / kCaWarps));
+    const dim3 grid((unsigned)a->Hq, (unsigned)a->V, (unsigned)a->B);
     SD_CUDA_CHECK(launch_pdl(d128 ? cache_merge_kernel<128> : cache_merge_kernel<64>, grid, dim3(kCaThreads), 0, cs, p),
                   "sd_cache_attend: merge launch");
     return launch_status(who);

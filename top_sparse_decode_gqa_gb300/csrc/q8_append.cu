@@ -9,9 +9,11 @@
 // Bound: HBM (each row is read once and written once at half or a quarter of its size), for a
 // few rows the launch.  A row is held in registers by d/8 lanes (8 elements a lane: one or two
 // 16-byte loads, one 8-byte store), so the maximum is a shuffle reduction and no row is read
-// twice; a warp loads kAppendRows row groups before it reduces any, which keeps 4 to 8 KB per warp in
-// flight.  The row index runs over (K or V, b, h, i) with i fastest: the rows a warp writes are
-// neighbours in the cache whatever the order of the source, whose rows are whole 128-byte lines.
+// twice.  A warp takes a block of neighbouring tokens of one head (8 at d = 128) and loads all of it before
+// it reduces any row: 2 KB of 16-bit rows in flight a warp, whole kilobytes written side by side.  Blocks
+// run over (sequence, tokens, K heads then V heads) with the head fastest, so that the CTAs at
+// work read neighbouring memory when the source is a projection's [B, n, heads, d] output.  The
+// 2 divisions of each of a block's 8 rows are one division instruction sequence, a lane each.
 #include <cuda_fp8.h>
 
 #include "sd_common.cuh"
@@ -31,8 +33,8 @@ struct AppendParams {
     const int32_t* pos0;
     const int32_t* count;
     int32_t* err;
-    int B, Hkv, n, T;
-    unsigned rows;  // B * Hkv * n
+    int Hkv, n, T;
+    unsigned nb, tasks;  // token blocks of a sequence; B * nb * 2 * Hkv
 };
 
 template <int SRC>  // 8 elements of a row in fp32 (sd_dtype)
@@ -77,60 +79,70 @@ SD_DEVINL uint32_t pack_e4m3(float a, float b, float c, float d) {
 template <int SRC, bool E4M3, int D, int U>
 __global__ void __launch_bounds__(kAppendThreads) q8_append_kernel(const AppendParams p) {
     constexpr int kLanes = D / 8;              // lanes of a row
-    constexpr int kPerWarp = 32 / kLanes;      // rows a warp holds at once
+    constexpr int kPerWarp = 32 / kLanes;      // rows a warp loads at once
     constexpr int kEs = SRC == SD_F32 ? 4 : 2;
+    const int lane = threadIdx.x & 31, sub = lane / kLanes, col = lane % kLanes;
+    const unsigned task = blockIdx.x * (kAppendThreads / 32) + (threadIdx.x >> 5);
+    if (task >= p.tasks) return;
+    const unsigned heads = 2u * (unsigned)p.Hkv;
+    const unsigned blk = task / heads, hv = task - blk * heads;
+    const unsigned b = blk / p.nb, i0 = (blk - b * p.nb) * (U * kPerWarp);
+    const int kv = hv >= (unsigned)p.Hkv ? 1 : 0;
+    const unsigned h = hv - (kv ? (unsigned)p.Hkv : 0u);
     pdl_wait();  // the new rows may come from the preceding kernel
     pdl_launch_dependents();
-    const int lane = threadIdx.x & 31, sub = lane / kLanes, col = lane % kLanes;
-    const unsigned warp = blockIdx.x * (kAppendThreads / 32) + (threadIdx.x >> 5);
-    const unsigned total = 2u * p.rows;
+    const int first = p.pos0[b], cnt = min(p.n, p.count != nullptr ? p.count[b] : p.n);
+    const long long sn = kv ? p.sn[1] : p.sn[0];
+    const uint8_t* src = (kv ? p.src[1] : p.src[0]) +
+                         ((long long)b * (kv ? p.sb[1] : p.sb[0]) + (long long)h * (kv ? p.sh[1] : p.sh[0]) + col * 8) * kEs;
     Eight<SRC> x[U];
-    long long dst[U];  // destination row, or -1
-    int which[U];
+    bool on[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        const unsigned r = (warp * U + u) * kPerWarp + sub;
-        dst[u] = -1;
-        which[u] = 0;
-        x[u].zero();
-        if (r < total) {
-            const int kv = r >= p.rows ? 1 : 0;
-            const unsigned rr = r - (kv ? p.rows : 0u);
-            const unsigned g = rr / (unsigned)p.n, i = rr - g * (unsigned)p.n;
-            const unsigned b = g / (unsigned)p.Hkv, h = g - b * (unsigned)p.Hkv;
-            const int cnt = p.count != nullptr ? p.count[b] : p.n;
-            if ((int)i < cnt) {
-                const long long pos = (long long)p.pos0[b] + i;
-                if (pos < 0 || pos >= p.T) {
-                    if (col == 0) report(p.err, SD_DEVERR_INDEX);
-                } else {
-                    dst[u] = (long long)g * p.T + pos;
-                    which[u] = kv;
-                    const uint8_t* s = kv ? p.src[1] : p.src[0];
-                    const long long off = (long long)b * (kv ? p.sb[1] : p.sb[0]) +
-                                          (long long)h * (kv ? p.sh[1] : p.sh[0]) +
-                                          (long long)i * (kv ? p.sn[1] : p.sn[0]) + col * 8;
-                    x[u].load(s + off * kEs);
-                }
-            }
+        const int i = (int)i0 + u * kPerWarp + sub;
+        const long long pos = (long long)first + i;
+        on[u] = i < cnt;
+        if (on[u] && (pos < 0 || pos >= p.T)) {
+            if (col == 0) report(p.err, SD_DEVERR_INDEX);
+            on[u] = false;
         }
+        if (on[u])
+            x[u].load(src + i * sn * kEs);
+        else
+            x[u].zero();
     }
+    float a[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         float f[8];
         x[u].get(f);
-        float a = 0.f;
+        a[u] = 0.f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) a = fmaxf(a, fabsf(f[j]));
+        for (int j = 0; j < 8; ++j) a[u] = fmaxf(a[u], fabsf(f[j]));
+    }
 #pragma unroll
-        for (int o = kLanes / 2; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-        if (dst[u] < 0) continue;
-        const float top = E4M3 ? 448.f : 127.f;
-        const bool zero = a < kAppendTiny;
-        const float inv = zero ? 0.f : __fdiv_rn(top, a);
-        const float scale = zero ? 0.f : __fdiv_rn(a, top);
+    for (int o = kLanes / 2; o > 0; o >>= 1)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = zero ? 0.f : __fmul_rn(f[j], inv);
+        for (int u = 0; u < U; ++u) a[u] = fmaxf(a[u], __shfl_xor_sync(0xffffffffu, a[u], o));
+    // lane 2u of a row's lanes divides top / a[u], lane 2u + 1 a[u] / top (a row below the smallest kept: 0)
+    constexpr float top = E4M3 ? 448.f : 127.f;
+    float mine = a[0];
+#pragma unroll
+    for (int u = 1; u < U; ++u) mine = (col >> 1) == u ? a[u] : mine;
+    const bool odd = (col & 1) != 0;
+    float r = __fdiv_rn(odd ? mine : top, odd ? top : mine);
+    if (mine < kAppendTiny) r = 0.f;
+    uint8_t* out = kv ? p.codes[1] : p.codes[0];
+    float* scale = kv ? p.scale[1] : p.scale[0];
+    const long long row0 = ((long long)b * p.Hkv + h) * p.T + first + (int)i0 + sub;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const float inv = __shfl_sync(0xffffffffu, r, sub * kLanes + 2 * u);
+        if (!on[u]) continue;
+        float f[8];
+        x[u].get(f);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = __fmul_rn(f[j], inv);
         uint2 c;
         if constexpr (E4M3) {
             c.x = pack_e4m3(f[0], f[1], f[2], f[3]);
@@ -139,29 +151,35 @@ __global__ void __launch_bounds__(kAppendThreads) q8_append_kernel(const AppendP
             c.x = pack_int8(f[0], f[1], f[2], f[3]);
             c.y = pack_int8(f[4], f[5], f[6], f[7]);
         }
-        uint8_t* out = which[u] ? p.codes[1] : p.codes[0];
-        *reinterpret_cast<uint2*>(out + dst[u] * D + col * 8) = c;
-        if (col == 0) (which[u] ? p.scale[1] : p.scale[0])[dst[u]] = scale;
+        const long long row = row0 + u * kPerWarp;
+        *reinterpret_cast<uint2*>(out + row * D + col * 8) = c;
+        if (col == 2 * u + 1) scale[row] = r;
     }
 }
 
+template <int SRC, bool E4M3, int D, int U>
+cudaError_t append_launch_u(AppendParams p, int B, cudaStream_t st) {
+    constexpr int kBlock = U * (32 / (D / 8)), kWarps = kAppendThreads / 32;
+    p.nb = ((unsigned)p.n + kBlock - 1) / kBlock;
+    p.tasks = (unsigned)B * p.nb * 2u * (unsigned)p.Hkv;
+    return launch_pdl(q8_append_kernel<SRC, E4M3, D, U>, dim3((p.tasks + kWarps - 1) / kWarps), dim3(kAppendThreads), 0, st,
+                      p);
+}
+
 template <int SRC, bool E4M3, int D>
-cudaError_t append_launch(const AppendParams& p, cudaStream_t st) {
-    constexpr int kPerWarp = 32 / (D / 8), kWarps = kAppendThreads / 32;
-    const unsigned total = 2u * p.rows;
-    // Four rows a lane in flight once every SM has work at that, else one (a decode step's few
-    // rows: 8192 warps hide the latency of one load, and 128 rows want 64 warps, not 16).
-    const bool many = total >= (unsigned)num_sms() * kWarps * kPerWarp * 4;
-    const unsigned per = kWarps * kPerWarp * (many ? 4u : 1u);
-    const unsigned grid = (total + per - 1) / per;
-    return many ? launch_pdl(q8_append_kernel<SRC, E4M3, D, 4>, dim3(grid), dim3(kAppendThreads), 0, st, p)
-                : launch_pdl(q8_append_kernel<SRC, E4M3, D, 1>, dim3(grid), dim3(kAppendThreads), 0, st, p);
+cudaError_t append_launch(const AppendParams& p, int B, cudaStream_t st) {
+    // Blocks of 4 loads a lane once every SM has two CTAs of such blocks, else of one (a decode
+    // step's 128 rows are then 64 to 128 warps' work, not 16).
+    constexpr int kBlock = 4 * (32 / (D / 8)), kWarps = kAppendThreads / 32;
+    const long long many = (long long)B * ((p.n + kBlock - 1) / kBlock) * 2 * p.Hkv;
+    return many >= 2LL * num_sms() * kWarps ? append_launch_u<SRC, E4M3, D, 4>(p, B, st)
+                                            : append_launch_u<SRC, E4M3, D, 1>(p, B, st);
 }
 
 template <int SRC>
-cudaError_t append_dispatch(const AppendParams& p, bool e4m3, int d, cudaStream_t st) {
-    if (e4m3) return d == 128 ? append_launch<SRC, true, 128>(p, st) : append_launch<SRC, true, 64>(p, st);
-    return d == 128 ? append_launch<SRC, false, 128>(p, st) : append_launch<SRC, false, 64>(p, st);
+cudaError_t append_dispatch(const AppendParams& p, int B, bool e4m3, int d, cudaStream_t st) {
+    if (e4m3) return d == 128 ? append_launch<SRC, true, 128>(p, B, st) : append_launch<SRC, true, 64>(p, B, st);
+    return d == 128 ? append_launch<SRC, false, 128>(p, B, st) : append_launch<SRC, false, 64>(p, B, st);
 }
 
 }  // namespace
@@ -182,6 +200,7 @@ extern "C" sd_status sd_q8_append(const sd_q8_append_args* a, void* stream) {
         return SD_ERR_UNSUPPORTED;
     }
     SD_REQUIRE((double)a->B * a->Hkv * a->n < 1073741824.0, "%s: B*Hkv*n must be below 2^30", who);
+    SD_REQUIRE(a->Hkv <= 65535, "%s: Hkv must be <= 65535", who);
     if (a->B == 0 || a->n == 0) return SD_OK;
     SD_REQUIRE(a->k_new && a->v_new && a->k_codes && a->v_codes && a->k_scale && a->v_scale && a->pos0,
                "%s: null pointer", who);
@@ -206,16 +225,14 @@ extern "C" sd_status sd_q8_append(const sd_q8_append_args* a, void* stream) {
     p.pos0 = a->pos0;
     p.count = a->count;
     p.err = a->err_word;
-    p.B = a->B;
     p.Hkv = a->Hkv;
     p.n = a->n;
     p.T = a->T;
-    p.rows = (unsigned)a->B * a->Hkv * a->n;
     const bool e4m3 = a->code_dtype == SD_E4M3;
     cudaStream_t st = as_stream(stream);
-    cudaError_t e = a->dtype == SD_F32   ? append_dispatch<SD_F32>(p, e4m3, a->d, st)
-                    : a->dtype == SD_F16 ? append_dispatch<SD_F16>(p, e4m3, a->d, st)
-                                         : append_dispatch<SD_BF16>(p, e4m3, a->d, st);
+    cudaError_t e = a->dtype == SD_F32   ? append_dispatch<SD_F32>(p, a->B, e4m3, a->d, st)
+                    : a->dtype == SD_F16 ? append_dispatch<SD_F16>(p, a->B, e4m3, a->d, st)
+                                         : append_dispatch<SD_BF16>(p, a->B, e4m3, a->d, st);
     SD_CUDA_CHECK(e, "sd_q8_append: launch");
     return launch_status(who);
 }

@@ -10,11 +10,13 @@
 // loads.  One cluster of up to 8 CTAs takes a sequence.  Every warp owns one contiguous part of the
 // row and sums it; the warps' sums meet through distributed shared memory, so every CTA knows
 // which warp's part holds the crossing, and the CTA of that warp reads the part again (from
-// L2) to find the token.  The weights are summed as integers in units of 2^-56 (each p and q is truncated
-// to such a multiple, which is exact down to 2^-33): the sums do not depend on the order of
-// additions, so neither do the results, and a fp32 sum's rounding would move the crossing past
-// a token of 1e-5 probability about once in a thousand draws.  The integers take fewer instructions
-// than fp64 sums, whose rate is 1/64 of the fp32 rate here.
+// L2) to find the token.  The weights are summed as integers in units of 2^-45 (each p and q is
+// rounded to the nearest such multiple): the sums do not depend on the order of additions, so neither do the
+// results; a fp32 sum's rounding would move the crossing past a token of 1e-5 probability about
+// once in a thousand draws, this rounding (2^-39 over a row of 131072) about once in 10^6.
+// Integers by two fp32 additions of a constant, whose sum's low bits are the multiple, and integer adds: 4 to 5
+// instructions at full rate for each probability, where shifting its mantissa took 14 and a fp64 sum
+// runs at 1/64 of the fp32 rate.
 #include <cooperative_groups.h>
 #include <cuda_fp16.h>
 
@@ -29,6 +31,7 @@ namespace {
 constexpr int kVdThreads = 512;
 constexpr int kVdWarps = kVdThreads / 32;
 constexpr int kVdMaxCtas = 8;
+constexpr int kVdBatch = 4;    // groups of four entries a lane loads at once
 constexpr int kVdPart = 4096;  // entries of a row that make a CTA of its own worth while
 
 struct VerifyParams {
@@ -44,15 +47,22 @@ struct VerifyParams {
     int V, N, ctas, vec;
 };
 
-// A probability in units of 2^-56, truncated: mantissa * 2^(e - 150 + 56).
-SD_DEVINL unsigned long long fixed56(float x) {
+// A probability in [0, 1] as hi * 2^-22 + lo * 2^-45: x + 3 lies in [3, 4], where a fp32 number's last
+// bit is 2^-22, so its bits less those of 3.0 are hi; what is left, at most 2^-23, likewise.
+struct Fixed {
+    int hi, lo;
+};
+constexpr float kFixA = 3.f, kFixB = 3.5762786865234375e-07f;  // 3, 1.5 * 2^-22
+SD_DEVINL Fixed fixed45(float x) {
     x = fminf(fmaxf(x, 0.f), 1.f);  // (a NaN becomes 0: fmaxf takes the other operand)
-    const uint32_t u = __float_as_uint(x);
-    const int e = (int)(u >> 23), sh = e - 94;
-    if (e == 0) return 0ull;
-    const unsigned long long m = (u & 0x7fffffu) | 0x800000u;
-    return sh >= 0 ? m << sh : (sh > -24 ? m >> -sh : 0ull);
+    const float y = __fadd_rn(x, kFixA);
+    const float z = __fadd_rn(__fsub_rn(x, __fsub_rn(y, kFixA)), kFixB);
+    Fixed f;
+    f.hi = __float_as_int(y) - __float_as_int(kFixA);
+    f.lo = __float_as_int(z) - __float_as_int(kFixB);
+    return f;
 }
+SD_DEVINL long long joined(int hi, int lo) { return ((long long)hi << 23) + lo; }
 
 template <int DT>
 SD_DEVINL float prob_at(const void* base, size_t i) {
@@ -93,19 +103,50 @@ struct Weights {
     size_t prow, qrow;
     int skip, N;
     bool vec;
+    SD_DEVINL Fixed one(float a, float b, int i) const {
+        Fixed x = fixed45(a);
+        if (q != nullptr) {
+            const Fixed y = fixed45(b);
+            x.hi -= y.hi;
+            x.lo -= y.lo;
+            if (!(a > b)) x.hi = x.lo = 0;
+        }
+        if (i == skip) x.hi = x.lo = 0;
+        return x;
+    }
     SD_DEVINL void four(int i, unsigned long long (&w)[4]) const {
-        float a[4], b[4];
+        float a[4], b[4] = {};
         prob4<DT>(p, prow, i, N, vec, a);
         if (q != nullptr) prob4<DT>(q, qrow, i, N, vec, b);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            unsigned long long x = fixed56(a[j]);
-            if (q != nullptr) {
-                const unsigned long long y = fixed56(b[j]);
-                x = x > y ? x - y : 0ull;
-            }
-            w[j] = i + j == skip ? 0ull : x;
+            const Fixed f = one(a[j], b[j], i + j);
+            w[j] = (unsigned long long)joined(f.hi, f.lo);
         }
+    }
+    // the sum of the weights of K groups of four, i, i + 128, .., all loaded before any is summed
+    template <int K>
+    SD_DEVINL unsigned long long sum(int i, int hi_end) const {
+        float a[K][4], b[K][4];
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) a[k][j] = b[k][j] = 0.f;
+            if (i + 128 * k < hi_end) {
+                prob4<DT>(p, prow, i + 128 * k, N, vec, a[k]);
+                if (q != nullptr) prob4<DT>(q, qrow, i + 128 * k, N, vec, b[k]);
+            }
+        }
+        int hi = 0, lo = 0;  // 4 K terms of at most 2^22 each
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const Fixed f = one(a[k][j], b[k][j], i + 128 * k + j);
+                hi += f.hi;
+                lo += f.lo;
+            }
+        return (unsigned long long)joined(hi, lo);
     }
 };
 
@@ -145,12 +186,13 @@ __global__ void __launch_bounds__(kVdThreads) verify_kernel(const VerifyParams p
             bool no = false;
             if (i < n) {
                 const int x = p.draft[(size_t)b * V + i];
+                const float u = p.u[(size_t)b * V + i];
                 no = true;
                 if (x >= 0 && x < N) {
                     // products of two fp32 numbers are exact in fp64
                     const double px = prob_at<DT>(p.p, ((size_t)b * (V + 1) + i) * N + x);
                     const double qx = p.q != nullptr ? prob_at<DT>(p.q, ((size_t)b * V + i) * N + x) : 1.f;
-                    no = !((double)p.u[(size_t)b * V + i] * qx < px);
+                    no = !((double)u * qx < px);
                 } else if (rank == 0) {
                     report(p.err, SD_DEVERR_INDEX);
                 }
@@ -177,12 +219,7 @@ __global__ void __launch_bounds__(kVdThreads) verify_kernel(const VerifyParams p
     for (int mode = 0;; ++mode) {
         const long lo = (long)k * part, hi = min((long)N, lo + part);
         unsigned long long sum = 0ull;
-#pragma unroll 4
-        for (long i = lo + 4 * lane; i < hi; i += 128) {
-            unsigned long long x[4];
-            w.four((int)i, x);
-            sum += (x[0] + x[1]) + (x[2] + x[3]);
-        }
+        for (long i = lo + 4 * lane; i < hi; i += 128 * kVdBatch) sum += w.template sum<kVdBatch>((int)i, (int)hi);
         sum = warp_sum_u64(sum);
         if (lane == 0) wsum[warp] = sum;
         cluster.sync();
