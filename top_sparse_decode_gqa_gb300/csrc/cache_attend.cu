@@ -126,6 +126,8 @@ SD_DEVINL void mma16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint3
 SD_DEVINL uint4 ld_row16(const uint8_t* p) { return __ldg(reinterpret_cast<const uint4*>(p)); }
 SD_DEVINL uint2 ld_row8(const uint8_t* p) { return __ldg(reinterpret_cast<const uint2*>(p)); }
 
+SD_DEVINL void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
 // What a lane holds of a step's 16 rows.
 template <int KIND, int D>
 struct Rows {
@@ -341,11 +343,12 @@ SD_DEVINL void ca_output(const Rows<KIND, D>& rw, const float (&s)[NQ][4], CaSta
             if constexpr (HILO) pl[nq][h] = movmatrix_t(lo);
         }
     auto pv = [&](int md, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+        if constexpr (HILO) {
 #pragma unroll
-        for (int nq = 0; nq < NQ; ++nq) {
-            if constexpr (HILO) mma16<F16>(st.o[md][nq], a0, a1, a2, a3, pl[nq][0], pl[nq][1]);
-            mma16<F16>(st.o[md][nq], a0, a1, a2, a3, ph[nq][0], ph[nq][1]);
+            for (int nq = 0; nq < NQ; ++nq) mma16<F16>(st.o[md][nq], a0, a1, a2, a3, pl[nq][0], pl[nq][1]);
         }
+#pragma unroll
+        for (int nq = 0; nq < NQ; ++nq) mma16<F16>(st.o[md][nq], a0, a1, a2, a3, ph[nq][0], ph[nq][1]);
     };
 #pragma unroll
     for (int w = 0; w < Rows<KIND, D>::kVw; ++w) {
@@ -398,6 +401,7 @@ struct CaShared {
     float o[kCaWarps][8 * NQ][kPitch];
     float2 ml[kCaWarps][8 * NQ];
     uint2 q[NQ >= 2 ? D / 16 * NQ * 32 : 1];
+    float qs[8 * NQ];
     int lim[8 * NQ];
     unsigned part[kCaWarps], base;
     int b;
@@ -484,73 +488,6 @@ __global__ void __launch_bounds__(kCaThreads, MINB) cache_attend_kernel(const Ca
         const int list = SEL ? p.n_list : len;
         const int j0 = (int)j * kCaTile, j1 = len == 0 ? j0 : min(list, j0 + (int)seg * kCaTile);
 
-        // the query rows 8nq + g8 as B fragments, their limits and the smallest limit
-        Queries<D, NQ> q;
-        q.sh = sh.q;
-        __syncthreads();  // (the segment before is done with the limits and the states)
-        int lmin = p.T;  // rows every query sees
-        if (tid < 8 * NQ) sh.lim[tid] = tid < p.R ? min(p.qpos[(size_t)b * p.V + tid / p.G], p.T - 1) : -1;
-        for (int v = 0; v < p.V; ++v) lmin = min(lmin, p.qpos[(size_t)b * p.V + v] + 1);
-#pragma unroll
-        for (int nq = 0; nq < NQ; ++nq) {
-            const int r = 8 * nq + g8;
-            const bool have = r < p.R;
-            const int v = have ? r / p.G : 0, gi = have ? r - v * p.G : 0;
-            const uint8_t* qrow = p.q + (((size_t)b * p.V + v) * p.Hq + (size_t)kvh * p.G + gi) * (D * 2);
-            uint32_t raw[kMd][2];
-            if constexpr (F16) {
-                uint32_t top = 0u;
-#pragma unroll
-                for (int cc = 0; cc < Rows<KIND, D>::kKc; ++cc)
-#pragma unroll
-                    for (int hh = 0; hh < 2; ++hh) {  // dims 64 cc + 16 t4 + 8 hh ..
-                        const uint4 x = have ? ld_row16(qrow + 2 * (64 * cc + 16 * t4 + 8 * hh)) : make_uint4(0u, 0u, 0u, 0u);
-                        raw[4 * cc + 2 * hh][0] = x.x;
-                        raw[4 * cc + 2 * hh][1] = x.y;
-                        raw[4 * cc + 2 * hh + 1][0] = x.z;
-                        raw[4 * cc + 2 * hh + 1][1] = x.w;
-                        top = max(top, max(max(x.x & 0x7fff0000u, (x.x << 16) & 0x7fff0000u),
-                                           max(x.y & 0x7fff0000u, (x.y << 16) & 0x7fff0000u)));
-                        top = max(top, max(max(x.z & 0x7fff0000u, (x.z << 16) & 0x7fff0000u),
-                                           max(x.w & 0x7fff0000u, (x.w << 16) & 0x7fff0000u)));
-                    }
-                top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                const uint32_t e = min(max(top >> 23, 1u), 253u);
-                const float down = __uint_as_float((254u - e) << 23), up = __uint_as_float(e << 23);
-#pragma unroll
-                for (int k = 0; k < kMd; ++k)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        raw[k][i] = pack_f16x2(bf16lo(raw[k][i]) * down, bf16hi(raw[k][i]) * down);
-#pragma unroll
-                for (int e2 = 0; e2 < 2; ++e2)
-                    q.qs[nq][e2] = __shfl_sync(0xffffffffu, up * p.scale_log2, (2 * t4 + e2) * 4);
-            } else {
-#pragma unroll
-                for (int cc = 0; cc < Rows<KIND, D>::kKc; ++cc) {  // dims 32 cc + 8 t4 ..
-                    const uint4 x = have ? ld_row16(qrow + 2 * (32 * cc + 8 * t4)) : make_uint4(0u, 0u, 0u, 0u);
-                    raw[2 * cc][0] = x.x;
-                    raw[2 * cc][1] = x.y;
-                    raw[2 * cc + 1][0] = x.z;
-                    raw[2 * cc + 1][1] = x.w;
-                }
-                q.qs[nq][0] = q.qs[nq][1] = p.scale_log2;
-            }
-#pragma unroll
-            for (int k = 0; k < kMd; ++k) {
-                if constexpr (Queries<D, NQ>::kShared) {
-                    if (warp == nq) sh.q[(k * NQ + nq) * 32 + lane] = make_uint2(raw[k][0], raw[k][1]);
-                } else {
-                    q.f[k][nq][0] = raw[k][0];
-                    q.f[k][nq][1] = raw[k][1];
-                }
-            }
-        }
-        __syncthreads();
-
-        CaState<D, NQ> st;
-        st.init();
         const uint8_t* kbase = p.kc + (size_t)g * p.T * kRow;
         const uint8_t* vbase = p.vc + (size_t)g * p.T * kRow;
         const float* ksb = p.ks + (size_t)g * p.T;
@@ -616,6 +553,104 @@ __global__ void __launch_bounds__(kCaThreads, MINB) cache_attend_kernel(const Ca
                 }
             }
         };
+        // asks L2 for the rows of a step (lane l: K row l, lane 16 + l: V row l) and their scales
+        auto ahead = [&](int step, int rows) {
+            const int i = j0 + 16 * step + (lane & 15);
+            const int t = SEL ? rows : i;
+            if (SEL ? t < 0 : i >= j1) return;
+            const uint8_t* at = (lane < 16 ? kbase : vbase) + (size_t)t * kRow;
+            prefetch_l2(at);
+            if constexpr (kRow > 128) prefetch_l2(at + 128);
+            if constexpr (F16) {
+                if (SEL || (lane & 15) == 0) prefetch_l2((lane < 16 ? ksb : vsb) + t);
+            }
+        };
+
+        const int nsteps = (j1 - j0 + 15) / 16;
+        int rows = -1, next = -1;
+        if (warp < nsteps) {  // the first rows are on their way while the queries are prepared
+            if constexpr (SEL) {
+                rows = resolve(warp);
+                next = resolve(warp + kCaWarps);
+            }
+            fetch_k(warp, rows);
+            fetch_v(warp, rows);
+            ahead(warp + kCaWarps, next);
+            if constexpr (!SEL) ahead(warp + 2 * kCaWarps, 0);
+        }
+
+        // the query rows 8nq + g8 as B fragments, their limits and the smallest limit
+        Queries<D, NQ> q;
+        q.sh = sh.q;
+        __syncthreads();  // (the segment before is done with the limits and the states)
+        int lmin = p.T;  // rows every query sees
+        if (tid < 8 * NQ) sh.lim[tid] = tid < p.R ? min(p.qpos[(size_t)b * p.V + tid / p.G], p.T - 1) : -1;
+        for (int v = 0; v < p.V; ++v) lmin = min(lmin, p.qpos[(size_t)b * p.V + v] + 1);
+#pragma unroll
+        for (int nq = 0; nq < NQ; ++nq) {
+            if (Queries<D, NQ>::kShared && warp != nq) continue;  // tile nq is warp nq's to prepare
+            const int r = 8 * nq + g8;
+            const bool have = r < p.R;
+            const int v = have ? r / p.G : 0, gi = have ? r - v * p.G : 0;
+            const uint8_t* qrow = p.q + (((size_t)b * p.V + v) * p.Hq + (size_t)kvh * p.G + gi) * (D * 2);
+            uint32_t raw[kMd][2];
+            if constexpr (F16) {
+                uint32_t top = 0u;
+#pragma unroll
+                for (int cc = 0; cc < Rows<KIND, D>::kKc; ++cc)
+#pragma unroll
+                    for (int hh = 0; hh < 2; ++hh) {  // dims 64 cc + 16 t4 + 8 hh ..
+                        const uint4 x = have ? ld_row16(qrow + 2 * (64 * cc + 16 * t4 + 8 * hh)) : make_uint4(0u, 0u, 0u, 0u);
+                        raw[4 * cc + 2 * hh][0] = x.x;
+                        raw[4 * cc + 2 * hh][1] = x.y;
+                        raw[4 * cc + 2 * hh + 1][0] = x.z;
+                        raw[4 * cc + 2 * hh + 1][1] = x.w;
+                        top = max(top, max(max(x.x & 0x7fff0000u, (x.x << 16) & 0x7fff0000u),
+                                           max(x.y & 0x7fff0000u, (x.y << 16) & 0x7fff0000u)));
+                        top = max(top, max(max(x.z & 0x7fff0000u, (x.z << 16) & 0x7fff0000u),
+                                           max(x.w & 0x7fff0000u, (x.w << 16) & 0x7fff0000u)));
+                    }
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                const uint32_t e = min(max(top >> 23, 1u), 253u);
+                const float down = __uint_as_float((254u - e) << 23), up = __uint_as_float(e << 23);
+#pragma unroll
+                for (int k = 0; k < kMd; ++k)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        raw[k][i] = pack_f16x2(bf16lo(raw[k][i]) * down, bf16hi(raw[k][i]) * down);
+                if (t4 == 0) sh.qs[r] = up * p.scale_log2;
+            } else {
+#pragma unroll
+                for (int cc = 0; cc < Rows<KIND, D>::kKc; ++cc) {  // dims 32 cc + 8 t4 ..
+                    const uint4 x = have ? ld_row16(qrow + 2 * (32 * cc + 8 * t4)) : make_uint4(0u, 0u, 0u, 0u);
+                    raw[2 * cc][0] = x.x;
+                    raw[2 * cc][1] = x.y;
+                    raw[2 * cc + 1][0] = x.z;
+                    raw[2 * cc + 1][1] = x.w;
+                }
+                if (t4 == 0) sh.qs[r] = p.scale_log2;
+            }
+#pragma unroll
+            for (int k = 0; k < kMd; ++k) {
+                if constexpr (Queries<D, NQ>::kShared) {
+                    sh.q[(k * NQ + nq) * 32 + lane] = make_uint2(raw[k][0], raw[k][1]);
+                } else {
+                    q.f[k][nq][0] = raw[k][0];
+                    q.f[k][nq][1] = raw[k][1];
+                }
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int nq = 0; nq < NQ; ++nq) {
+            const float2 f = *reinterpret_cast<const float2*>(&sh.qs[8 * nq + 2 * t4]);
+            q.qs[nq][0] = f.x;
+            q.qs[nq][1] = f.y;
+        }
+
+        CaState<D, NQ> st;
+        st.init();
         // Folds the registers' state into the warp's in shared memory (all of it relative to the softmax
         // maximum m), and starts it anew.
         auto fold = [&](bool first) {
@@ -656,16 +691,8 @@ __global__ void __launch_bounds__(kCaThreads, MINB) cache_attend_kernel(const Ca
             st.clear();
         };
 
-        const int nsteps = (j1 - j0 + 15) / 16;
         bool first = true;
         if (warp < nsteps) {
-            int rows = -1, next = -1;
-            if constexpr (SEL) {
-                rows = resolve(warp);
-                next = resolve(warp + kCaWarps);
-            }
-            fetch_k(warp, rows);
-            fetch_v(warp, rows);
             int since = 0;
             for (int s = warp; s < nsteps; s += kCaWarps) {
                 const bool more = s + kCaWarps < nsteps;
@@ -698,6 +725,9 @@ __global__ void __launch_bounds__(kCaThreads, MINB) cache_attend_kernel(const Ca
                 if constexpr (SEL) {
                     rows = next;
                     next = resolve(s + 2 * kCaWarps);
+                    ahead(s + 2 * kCaWarps, next);
+                } else {
+                    ahead(s + 3 * kCaWarps, 0);
                 }
                 if (HILO && ++since == kFoldSteps) {
                     fold(first);

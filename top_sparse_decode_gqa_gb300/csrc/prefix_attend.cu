@@ -19,6 +19,9 @@
 // The MMA warp alternates the tiles, so the tensor cores work on one while the other's softmax
 // runs.  O_t is rescaled only when a row's maximum has grown by more than 2^8 since the last time
 // (weights stay below 2^8; the quotient O / l does not change), which is rare after the first tiles.
+// The tensor cores cut what they add to a sum (2^-24 of it), so SD_F32 output starts O_t anew every
+// 16 tiles and adds up in fp32 in the workspace (L2).  The softmax takes 4 to 5 instructions an
+// element: products and sums two at a time (f32x2), three-way maxima.
 // TMEM: S_0, S_1 (128 columns each), O_0, O_1 (d each).  Shared memory: 2 Q tiles, 2 stages of K
 // and of V.  Every wait is bounded; a wait that runs out raises an abort flag, the copies and MMAs
 // in flight land, and the kernel frees its TMEM and returns.
@@ -36,6 +39,7 @@ constexpr int kPfRows = 128;  // query rows a tile
 constexpr int kPfProd = 8, kPfMma = 9;  // warps 0-3 and 4-7: softmax of row tiles 0 and 1
 constexpr int kPfThreads = 32 * 10;
 constexpr int kPfStages = 2;
+constexpr int kPfFold = 16;      // key tiles after which SD_F32 output folds O
 constexpr float kPfGrow = 8.f;  // the growth of a row's maximum (base 2) that O is rescaled at
 
 template <int D>
@@ -59,6 +63,46 @@ struct PfParams {
     float scale_log2;
     unsigned long long wait_ns;
 };
+
+// Two fp32 operations in one instruction.
+SD_DEVINL uint64_t pack2(float x, float y) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+SD_DEVINL float2 unpack2(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+SD_DEVINL uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+SD_DEVINL uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+SD_DEVINL float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+// A bounded wait that gives up (within its limit) and raises the abort flag for the others.
+SD_DEVINL bool pf_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, uint64_t lim) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = globaltimer_ns();
+    for (uint32_t i = 1;; ++i) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if ((i & 63u) == 0u && (*abort_flag || globaltimer_ns() - t0 > lim)) {
+            *abort_flag = 1;
+            return false;
+        }
+    }
+}
 
 template <int D, bool HILO>
 __global__ void __launch_bounds__(kPfThreads, 1)
@@ -126,7 +170,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                 const int s = n % kPfStages;
                 const uint32_t ph = ((uint32_t)(n / kPfStages) & 1u) ^ 1u;
                 const int key = (n0 + n) * kPfKeys;
-                if (!ds_wait(&kempty[s], ph, abort_flag, lim)) {
+                if (!pf_wait(&kempty[s], ph, abort_flag, lim)) {
                     *abort_flag = 1;
                     break;
                 }
@@ -135,7 +179,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                 for (int a = 0; a < L::kAtoms; ++a)
                     tma_load_3d(sm + L::oK + s * L::kTile + a * L::kAtom, &kmap, 64 * a, key, kvh, &kfull[s]);
                 issued = 2 * n + 1;
-                if (!ds_wait(&vempty[s], ph, abort_flag, lim)) {
+                if (!pf_wait(&vempty[s], ph, abort_flag, lim)) {
                     *abort_flag = 1;
                     break;
                 }
@@ -167,11 +211,11 @@ __global__ void __launch_bounds__(kPfThreads, 1)
 #pragma unroll
                 for (int k = 0; k < kPfKeys / 16; ++k) {
                     const uint64_t bd = umma_desc_mn_sw128(b0 + k * 2048, L::kAtom);
-                    umma_bf16_ta(o, a + 8 * k, bd, kIdO, (n > 0 || k > 0) ? 1u : 0u);
+                    umma_bf16_ta(o, a + 8 * k, bd, kIdO, (HILO ? n % kPfFold : n) > 0 || k > 0 ? 1u : 0u);
                     if (HILO) umma_bf16_ta(o, a + 64 + 8 * k, bd, kIdO, 1u);
                 }
             };
-            bool ok = ds_wait(qfull, 0u, abort_flag, lim) && ds_wait(&kfull[0], 0u, abort_flag, lim);
+            bool ok = pf_wait(qfull, 0u, abort_flag, lim) && pf_wait(&kfull[0], 0u, abort_flag, lim);
             if (ok) {
                 tc_fence_after_sync();
                 for (int t = 0; t < nq; ++t) scores(t, 0);
@@ -180,10 +224,10 @@ __global__ void __launch_bounds__(kPfThreads, 1)
             for (int n = 0; ok && n < nt; ++n) {
                 const uint32_t ph = (uint32_t)(n / kPfStages) & 1u;
                 const uint32_t phn = (uint32_t)((n + 1) / kPfStages) & 1u;
-                ok = ds_wait(&vfull[n % kPfStages], ph, abort_flag, lim);
-                if (ok && n + 1 < nt) ok = ds_wait(&kfull[(n + 1) % kPfStages], phn, abort_flag, lim);
+                ok = pf_wait(&vfull[n % kPfStages], ph, abort_flag, lim);
+                if (ok && n + 1 < nt) ok = pf_wait(&kfull[(n + 1) % kPfStages], phn, abort_flag, lim);
                 for (int t = 0; ok && t < nq; ++t) {
-                    ok = ds_wait(&pfull[t], (uint32_t)n & 1u, abort_flag, lim);
+                    ok = pf_wait(&pfull[t], (uint32_t)n & 1u, abort_flag, lim);
                     if (!ok) break;
                     tc_fence_after_sync();
                     output(t, n);
@@ -206,14 +250,43 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         const uint32_t ts = tmem + lanes + t * 128, to = tmem + lanes + 256 + t * 128;
         const int r = quarter * 32 + lane;  // this thread's row of the tile
         const bool mine = r < p.G * p.bpt;
+        const long row = (long)(2 * pair + t) * p.G * p.bpt + r;
+        const bool store = mine && row < p.M;
+        const size_t at = ((size_t)kvh * p.splits + split) * p.M + (store ? row : 0);
         float m = -INFINITY, l = 0.f;
+        float fm = 0.f;       // the maximum that the folded sums in the workspace are relative to
+        bool folded = false;
+        // O_t of this row, added to what was folded before, to the workspace
+        auto write_o = [&]() {
+            const float f = folded ? fast_exp2(fm - m) : 0.f;
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+                uint32_t o[32];
+                tmem_ld32_nowait(to + 32 * c, o);
+                tmem_wait_ld();
+                if (store) {
+                    float4* dst = reinterpret_cast<float4*>(p.o + at * D + 32 * c);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        float4 x = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
+                                               __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
+                        if (HILO && folded) {
+                            const float4 y = dst[i];
+                            x = make_float4(fmaf(y.x, f, x.x), fmaf(y.y, f, x.y), fmaf(y.z, f, x.z), fmaf(y.w, f, x.w));
+                        }
+                        dst[i] = x;
+                    }
+                }
+            }
+            fm = m;
+            folded = true;
+        };
         bool ok = true;
         for (int n = 0; n < nt; ++n) {
-            if (!warp_wait(&sfull[t], (uint32_t)n & 1u, const_cast<volatile int*>(abort_flag), lim)) {
-                ok = false;
-                break;
-            }
+            ok = __all_sync(0xffffffffu, pf_wait(&sfull[t], (uint32_t)n & 1u, abort_flag, lim));
+            if (!ok) break;
             tc_fence_after_sync();
+            if (HILO && n > 0 && n % kPfFold == 0) write_o();
             uint32_t s[128];
 #pragma unroll
             for (int c = 0; c < 4; ++c) tmem_ld32_nowait(ts + 32 * c, s + 32 * c);
@@ -224,9 +297,13 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                 for (int i = 0; i < kPfKeys; ++i)
                     if (i >= valid) s[i] = 0xff800000u;  // -inf
             }
-            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            float mx[4];
 #pragma unroll
-            for (int i = 0; i < kPfKeys; ++i) mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(s[i]));
+            for (int j = 0; j < 4; ++j)
+                mx[j] = max3(__uint_as_float(s[3 * j]), __uint_as_float(s[3 * j + 1]), __uint_as_float(s[3 * j + 2]));
+#pragma unroll
+            for (int i = 12; i < kPfKeys; i += 2)
+                mx[(i >> 1) & 3] = max3(mx[(i >> 1) & 3], __uint_as_float(s[i]), __uint_as_float(s[i + 1]));
             const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
             // (rows past the tile's query rows hold whatever shared memory held: left alone)
             const float grown = mine && top > m + kPfGrow ? top : m;
@@ -247,49 +324,39 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                     tmem_st16(to + 32 * c + 16, o + 16);
                 }
             }
-            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+            uint64_t sum[2] = {0ull, 0ull};
+            const uint64_t c2 = pack2(p.scale_log2, p.scale_log2), m2 = pack2(-m, -m);
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 uint32_t hi[16], lo[16];
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    const float x = fast_exp2(fmaf(__uint_as_float(s[32 * c + 2 * i]), p.scale_log2, -m));
-                    const float y = fast_exp2(fmaf(__uint_as_float(s[32 * c + 2 * i + 1]), p.scale_log2, -m));
-                    sum[(2 * i) & 3] += x;
-                    sum[(2 * i + 1) & 3] += y;
-                    if constexpr (HILO)
-                        split_bf16x2(x, y, hi[i], lo[i]);
-                    else
-                        hi[i] = pack_bf16x2(x, y);
+                    const float2 z = unpack2(fma2(
+                        pack2(__uint_as_float(s[32 * c + 2 * i]), __uint_as_float(s[32 * c + 2 * i + 1])), c2, m2));
+                    const float x = fast_exp2(z.x), y = fast_exp2(z.y);
+                    const uint64_t xy = pack2(x, y);
+                    sum[i & 1] = add2(sum[i & 1], xy);
+                    hi[i] = pack_bf16x2(x, y);
+                    if constexpr (HILO) {  // what is left of the weights: x - hi is exact
+                        const float2 r = unpack2(fma2(pack2(bf16lo(hi[i]), bf16hi(hi[i])), pack2(-1.f, -1.f), xy));
+                        lo[i] = pack_bf16x2(r.x, r.y);
+                    }
                 }
                 tmem_st16(ts + 16 * c, hi);
                 if constexpr (HILO) tmem_st16(ts + 64 + 16 * c, lo);
             }
-            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            const float2 s2 = unpack2(add2(sum[0], sum[1]));
+            l += s2.x + s2.y;
             tmem_wait_st();
             tc_fence_before_sync();
             __syncwarp();
             if (lane == 0) mbar_arrive(&pfull[t]);
         }
-        if (ok) ok = warp_wait(&ofull[t], 0u, const_cast<volatile int*>(abort_flag), lim);
+        if (ok) ok = __all_sync(0xffffffffu, pf_wait(&ofull[t], 0u, abort_flag, lim));
         if (ok) {
             tc_fence_after_sync();
-            const long row = (long)(2 * pair + t) * p.G * p.bpt + r;
-            const bool store = mine && row < p.M;
-            const size_t at = ((size_t)kvh * p.splits + split) * p.M + (store ? row : 0);
+            write_o();
             if (store) p.ml[at] = make_float2(m, l);
-#pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-                uint32_t o[32];
-                tmem_ld32_nowait(to + 32 * c, o);
-                tmem_wait_ld();
-                if (store) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        reinterpret_cast<uint4*>(p.o + at * D + 32 * c)[i] =
-                            make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-                }
-            }
             tc_fence_before_sync();
         }
     }

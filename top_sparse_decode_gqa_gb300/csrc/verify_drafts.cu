@@ -165,7 +165,7 @@ SD_DEVINL unsigned long long warp_scan_u64(unsigned long long v, int lane) {
 }
 
 template <int DT>
-__global__ void __launch_bounds__(kVdThreads) verify_kernel(const VerifyParams p) {
+__global__ void __launch_bounds__(kVdThreads, 2) verify_kernel(const VerifyParams p) {
     namespace cg = cooperative_groups;
     cg::cluster_group cluster = cg::this_cluster();
     __shared__ unsigned long long wsum[kVdWarps];                 // this CTA's warps' sums (read by the cluster)
@@ -346,10 +346,9 @@ extern "C" sd_status sd_verify_drafts(const void* p, const void* q, sd_dtype dty
     a.V = V;
     a.N = N;
     a.vec = N % 4 == 0;  // then every row starts at a 4-entry boundary
-    // as many CTAs a sequence as fit on the GPU at once (four of 512 threads an SM), each with
-    // a part worth reading
+    // as many CTAs a sequence as fit on the GPU at once (two an SM), each with a part worth reading
     int C = kVdMaxCtas;
-    while (C > 1 && ((long)B * C > 4L * num_sms() || (N + C - 1) / C < kVdPart / 2)) C /= 2;
+    while (C > 1 && ((long)B * C > 2L * num_sms() || (N + C - 1) / C < kVdPart / 2)) C /= 2;
     a.ctas = C;
     cudaStream_t st = as_stream(stream);
     return dtype == SD_F32 ? verify_launch<SD_F32>(a, B, st)
