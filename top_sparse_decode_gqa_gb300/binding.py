@@ -7,6 +7,7 @@ a missing library is an error.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -774,16 +775,15 @@ def sd_cache_attend(args: sd_cache_attend_args, stream=None) -> None:
 
 
 def cache_attend(q, k_cache, v_cache, qpos, workspace=None, stream=None, **kw):
-    """Convenience wrapper: builds the args, sizes a workspace if none is given, runs the call
-    and returns (out, lse)."""
+    """Convenience wrapper: builds the args, makes a workspace if none is given (see
+    cache_attend_workspace), runs the call and returns (out, lse)."""
     a, out, lse = make_cache_attend_args(q, k_cache, v_cache, qpos, **kw)
-    need = sd_cache_attend_workspace_bytes(a)
-    if workspace is None or workspace.numel() * workspace.element_size() < need:
-        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
+    if workspace is None:
+        # made (for the allocator) on the stream of the call
+        with torch.cuda.stream(stream) if isinstance(stream, torch.cuda.Stream) else contextlib.nullcontext():
+            workspace = cache_attend_workspace(a)
     a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     sd_cache_attend(a, stream)
-    if stream is not None and hasattr(stream, "cuda_stream"):
-        workspace.record_stream(stream)  # a workspace made here may be freed before the stream is done
     return out, lse
 
 

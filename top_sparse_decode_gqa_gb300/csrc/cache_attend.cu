@@ -137,6 +137,7 @@ struct Rows {
     static constexpr int kVw = kRow / 32;     // 32-bit words of a V row a lane holds
     uint4 k[2][kKc];       // K rows g8 and g8 + 8, bytes 64c + 16 t4 ..
     float ks[2], vs[2];    // scales of rows g8 and g8 + 8
+    int pos[2];            // selected rows: their positions (INT_MAX: not attended by any query)
     uint32_t v[4][kVw];    // V rows 2 t4, 2 t4 + 1, 2 t4 + 8, 2 t4 + 9, columns g8 * D/8 ..
 
     SD_DEVINL void load_k(int h, const uint8_t* p) {  // p: the row's byte 16 t4
@@ -256,10 +257,11 @@ SD_DEVINL void ca_scores(const Rows<KIND, D>& rw, const Queries<D, NQ>& q, int l
     }
 }
 
-// The online softmax of a step: s becomes the weights of the V rows.  MASK: rows above a query's
-// limit (sl[8nq + 2t4 + e]) take no part (pos: the positions of rows g8, g8 + 8).
-template <int KIND, int D, int NQ, bool MASK>
-SD_DEVINL void ca_softmax(float (&s)[NQ][4], const float (&ks)[2], const float (&vs)[2], const int (&pos)[2],
+// The online softmax of a step: s becomes the weights of the V rows.  Unless every query sees all
+// rows of the step (all), those above a query's limit (sl[8nq + 2t4 + e]) take no part (pos: the
+// positions of rows g8, g8 + 8).
+template <int KIND, int D, int NQ>
+SD_DEVINL void ca_softmax(float (&s)[NQ][4], const float (&ks)[2], const float (&vs)[2], const int (&pos)[2], bool all,
                           const int* sl, int t4, const Queries<D, NQ>& q, CaState<D, NQ>& st) {
     constexpr bool F16 = KIND != kBf16;
     float top = -INFINITY, wide = 0.f;
@@ -282,9 +284,15 @@ SD_DEVINL void ca_softmax(float (&s)[NQ][4], const float (&ks)[2], const float (
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int e = i & 1, h = i >> 1;
-            const float x = s[nq][i] * (F16 ? ks[h] * q.qs[nq][e] : q.qs[nq][e]);
-            s[nq][i] = MASK && pos[h] > sl[8 * nq + 2 * t4 + e] ? -INFINITY : x;
+            s[nq][i] *= F16 ? ks[h] * q.qs[nq][e] : q.qs[nq][e];
         }
+    if (!all) {
+#pragma unroll
+        for (int nq = 0; nq < NQ; ++nq)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (pos[i >> 1] > sl[8 * nq + 2 * t4 + (i & 1)]) s[nq][i] = -INFINITY;
+    }
     weights();
     if (__any_sync(0xffffffffu, top > kGrow || wide > kLimF16)) {
 #pragma unroll
@@ -394,6 +402,69 @@ SD_DEVINL void store_pair(void* out, bool bf16, size_t i, float x, float y) {  /
         reinterpret_cast<float2*>(out)[i / 2] = make_float2(x, y);
 }
 
+// The sum of a query row's states start, start + step, ..: those of its group's runs (slots first ..
+// first + runs - 1) and of the prefix's splits.  Lane l holds columns kE l ..
+template <int D>
+struct RowSum {
+    static constexpr int kE = D / 32;
+    float acc[kE], L, top;
+};
+template <int D>
+SD_DEVINL RowSum<D> sum_states(const CaParams& p, int b, int kvh, int r, int first, int runs, int start, int step,
+                               int lane) {
+    constexpr int kE = RowSum<D>::kE;
+    const int n = runs + p.pre_splits;
+    const unsigned M = (unsigned)p.B * p.R, mrow = (unsigned)b * p.R + r;
+    auto ml_of = [&](int i) {
+        return __ldcg(i < runs ? &p.ws.ml[(size_t)(first + i) * p.R + r]
+                               : &p.ws.pre_ml[((size_t)kvh * p.pre_splits + (i - runs)) * M + mrow]);
+    };
+    auto o_of = [&](int i) {
+        return i < runs ? p.ws.o + ((size_t)(first + i) * p.R + r) * D
+                        : p.ws.pre_o + (((size_t)kvh * p.pre_splits + (i - runs)) * M + mrow) * D;
+    };
+    RowSum<D> s;
+    s.L = 0.f;
+    s.top = kNone;
+#pragma unroll
+    for (int e = 0; e < kE; ++e) s.acc[e] = 0.f;
+    for (int base = start; base < n; base += 32 * step) {
+        const int mine = base + step * lane;
+        const float2 ml = mine < n ? ml_of(mine) : make_float2(kNone, 0.f);
+        const float was = s.top;
+        s.top = fmaxf(was, warp_max(ml.x));
+        const float f = exp2f(fmaxf(ml.x, kNone) - s.top), fo = exp2f(was - s.top);
+        s.L = s.L * fo + ml.y * f;
+#pragma unroll
+        for (int e = 0; e < kE; ++e) s.acc[e] *= fo;
+        const int cnt = min(32, (n - base + step - 1) / step);
+        for (int k0 = 0; k0 < cnt; k0 += 8) {  // eight states' rows loaded together
+            float x[8][kE];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const float* o = o_of(base + step * min(k0 + k, cnt - 1)) + kE * lane;
+                if constexpr (kE == 4) {
+                    const float4 y = __ldcg(reinterpret_cast<const float4*>(o));
+                    x[k][0] = y.x, x[k][1] = y.y, x[k][2] = y.z, x[k][3] = y.w;
+                } else {
+                    const float2 y = __ldcg(reinterpret_cast<const float2*>(o));
+                    x[k][0] = y.x, x[k][1] = y.y;
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const float fk = __shfl_sync(0xffffffffu, f, min(k0 + k, 31));
+                if (k0 + k < cnt) {
+#pragma unroll
+                    for (int e = 0; e < kE; ++e) s.acc[e] = fmaf(x[k][e], fk, s.acc[e]);
+                }
+            }
+        }
+    }
+    s.L = warp_sum(s.L);
+    return s;
+}
+
 template <int D, int NQ>
 struct CaShared {
     // a state row: column g8 * D/8 + 2md + j at 18 md + 2 g8 + j
@@ -418,27 +489,37 @@ __global__ void __launch_bounds__(kCaThreads, MINB) cache_attend_kernel(const Ca
     auto& sh = *reinterpret_cast<CaShared<D, NQ>*>(ca_smem);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g8 = lane >> 2, t4 = lane & 3;
     const unsigned c = blockIdx.x;
-    pdl_wait();  // the cache, qpos and q may be the preceding kernels' results
+    // The cache, qpos and q may be the preceding kernels' results.  Behind a prefix kernel of the same
+    // call, which lets this one start only after its own wait for them, they are there already: the
+    // wait is then for that kernel alone, and comes before its states are read.
+    if (p.P == 0) pdl_wait();
     pdl_launch_dependents();
 
     // this CTA's run of units: [w0, w1) of all groups' units in order; no run is empty, so a
     // group's runs are in consecutive slots
     unsigned W, tb, j, w0;
     int b, kvh;
+    const bool few = p.B <= 32;  // lane i knows sequence i: no warp needs another
+    unsigned tl = 0u;
     if constexpr (SEL) {
         tb = tiles_of(p.n_list);
         W = (unsigned)p.B * p.Hkv * tb;
+    } else if (few) {
+        tl = lane < p.B ? tiles_of(seq_len(p, lane)) : 0u;
+        W = __reduce_add_sync(0xffffffffu, tl) * p.Hkv;
     } else {
         unsigned sum = 0;
         for (int i = tid; i < p.B; i += kCaThreads) sum += tiles_of(seq_len(p, i));
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        sum = __reduce_add_sync(0xffffffffu, sum);
         if (lane == 0) sh.part[warp] = sum;
         __syncthreads();
         W = (sh.part[0] + sh.part[1] + sh.part[2] + sh.part[3]) * p.Hkv;
     }
     const unsigned ncta = min(gridDim.x, W);
-    if (c >= ncta) return;
+    if (c >= ncta) {
+        if (p.P > 0) pdl_wait();  // (the merge kernel, where there is one, counts on the prefix being done)
+        return;
+    }
     const Cut cut(W, ncta);
     w0 = cut.start(c);
     const unsigned w1 = cut.start(c + 1);
@@ -447,6 +528,18 @@ __global__ void __launch_bounds__(kCaThreads, MINB) cache_attend_kernel(const Ca
         j = w0 - g * tb;
         b = (int)(g / (unsigned)p.Hkv);
         kvh = (int)(g - (unsigned)b * p.Hkv);
+    } else if (few) {
+        unsigned incl = tl;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const unsigned u = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += u;
+        }
+        b = __ffs((int)__ballot_sync(0xffffffffu, w0 < incl * p.Hkv)) - 1;
+        tb = __shfl_sync(0xffffffffu, tl, b);
+        const unsigned off = w0 - (__shfl_sync(0xffffffffu, incl, b) - tb) * p.Hkv;
+        kvh = (int)(off / tb);
+        j = off - (unsigned)kvh * tb;
     } else {
         // the sequence of unit w0: sequence i's units start at Hkv * (tiles before it)
         unsigned run = 0;
@@ -529,6 +622,10 @@ __global__ void __launch_bounds__(kCaThreads, MINB) cache_attend_kernel(const Ca
             } else {
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
+                    if constexpr (SEL) {
+                        const int t0 = __shfl_sync(0xffffffffu, rows, g8 + 8 * h);
+                        rw.pos[h] = t0 < 0 ? 0x7fffffff : t0;
+                    }
                     const int t = row_at(step, rows, g8 + 8 * h);
                     rw.load_k(h, kbase + (size_t)t * kRow + 16 * t4);
                     if constexpr (F16) {
@@ -568,15 +665,12 @@ __global__ void __launch_bounds__(kCaThreads, MINB) cache_attend_kernel(const Ca
 
         const int nsteps = (j1 - j0 + 15) / 16;
         int rows = -1, next = -1;
-        if (warp < nsteps) {  // the first rows are on their way while the queries are prepared
-            if constexpr (SEL) {
-                rows = resolve(warp);
-                next = resolve(warp + kCaWarps);
-            }
-            fetch_k(warp, rows);
-            fetch_v(warp, rows);
-            ahead(warp + kCaWarps, next);
-            if constexpr (!SEL) ahead(warp + 2 * kCaWarps, 0);
+        if constexpr (SEL) {
+            next = resolve(warp);
+            ahead(warp, next);
+        } else {
+            ahead(warp, 0);
+            ahead(warp + kCaWarps, 0);
         }
 
         // the query rows 8nq + g8 as B fragments, their limits and the smallest limit
@@ -691,52 +785,47 @@ __global__ void __launch_bounds__(kCaThreads, MINB) cache_attend_kernel(const Ca
             st.clear();
         };
 
+        // Pass s computes step s and fetches step s + 4, K rows as soon as the scores have used the last
+        // ones and V rows after the output (the first pass, s = warp - 4, only fetches).
         bool first = true;
-        if (warp < nsteps) {
-            int since = 0;
-            for (int s = warp; s < nsteps; s += kCaWarps) {
-                const bool more = s + kCaWarps < nsteps;
-                float sc[NQ][4];
+        int since = 0;
+        for (int s = warp - kCaWarps; s < nsteps; s += kCaWarps) {
+            const bool work = s >= 0, more = s + kCaWarps < nsteps;
+            if constexpr (SEL) {
+                rows = next;
+                next = resolve(s + 2 * kCaWarps);
+                ahead(s + 2 * kCaWarps, next);
+            } else {
+                ahead(s + 3 * kCaWarps, 0);
+            }
+            float sc[NQ][4], ks[2], vs[2];
+            int pos[2];
+            bool all = true;
+            if (work) {
                 ca_scores<KIND, D, NQ>(rw, q, lane, sc);
-                int pos[2];
                 if constexpr (SEL) {
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int t = __shfl_sync(0xffffffffu, rows, g8 + 8 * h);
-                        pos[h] = t < 0 ? 0x7fffffff : t;
-                    }
+                    pos[0] = rw.pos[0], pos[1] = rw.pos[1];
+                    all = __all_sync(0xffffffffu, max(pos[0], pos[1]) < lmin);
                 } else {
                     pos[0] = j0 + 16 * s + g8;
                     pos[1] = pos[0] + 8;
-                }
-                const float ks[2] = {rw.ks[0], rw.ks[1]}, vs[2] = {rw.vs[0], rw.vs[1]};
-                if (more) fetch_k(s + kCaWarps, next);
-                bool all = true;
-                if constexpr (SEL)
-                    all = __all_sync(0xffffffffu, max(pos[0], pos[1]) < lmin);
-                else
                     all = j0 + 16 * s + 16 <= lmin;
-                if (all)
-                    ca_softmax<KIND, D, NQ, false>(sc, ks, vs, pos, sh.lim, t4, q, st);
-                else
-                    ca_softmax<KIND, D, NQ, true>(sc, ks, vs, pos, sh.lim, t4, q, st);
+                }
+#pragma unroll
+                for (int h = 0; h < 2; ++h) ks[h] = rw.ks[h], vs[h] = rw.vs[h];
+            }
+            if (more) fetch_k(s + kCaWarps, rows);
+            if (work) {
+                ca_softmax<KIND, D, NQ>(sc, ks, vs, pos, all, sh.lim, t4, q, st);
                 ca_output<KIND, D, NQ, HILO>(rw, sc, st);
-                if (more) fetch_v(s + kCaWarps, next);
-                if constexpr (SEL) {
-                    rows = next;
-                    next = resolve(s + 2 * kCaWarps);
-                    ahead(s + 2 * kCaWarps, next);
-                } else {
-                    ahead(s + 3 * kCaWarps, 0);
-                }
-                if (HILO && ++since == kFoldSteps) {
-                    fold(first);
-                    first = false;
-                    since = 0;
-                }
+            }
+            if (more) fetch_v(s + kCaWarps, rows);
+            if (!more || (HILO && ++since > kFoldSteps)) {
+                fold(first);
+                first = false;
+                since = 1;
             }
         }
-        fold(first);
         __syncthreads();
         const bool whole = j == 0u && seg == tb && p.P == 0;
         const size_t slot = (size_t)c + g;
@@ -778,11 +867,13 @@ __global__ void __launch_bounds__(kCaThreads, MINB) cache_attend_kernel(const Ca
             if (!SEL && w < w1) tb = tiles_of(seq_len(p, b));
         }
     }
+    if (p.P > 0) pdl_wait();
 }
 
-// One CTA a query row: the states of its group's runs and of the prefix's splits into the output.
-// Each warp takes every fourth state; a row's states are loaded together, and the warps' sums
-// meet in shared memory in a fixed order.
+// One CTA a query row: every warp takes each fourth state, and the warps' sums meet in shared memory in
+// a fixed order.  (The last CTA of a group merging it instead of a second kernel was measured: it saves a
+// launch and loses more, since one CTA then does what 4 to 32 do here: 18.7 -> 22.4 us for the
+// selected blocks, 65 -> 77 us for 64 sequences behind a prefix of 32768.)
 template <int D>
 __global__ void __launch_bounds__(kCaThreads) cache_merge_kernel(const CaParams p) {
     __shared__ float so[kCaWarps][D];
@@ -790,68 +881,22 @@ __global__ void __launch_bounds__(kCaThreads) cache_merge_kernel(const CaParams 
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int h = (int)blockIdx.x, v = (int)blockIdx.y, b = (int)blockIdx.z;
     const int kvh = h / p.G, gi = h - kvh * p.G, r = v * p.G + gi;
-    const unsigned M = (unsigned)p.B * p.R, mrow = ((unsigned)b * p.V + v) * p.G + gi;
     pdl_wait();
     pdl_launch_dependents();
     const int2 own = p.ws.meta[b * p.Hkv + kvh];
-    const int n = own.y + p.pre_splits;
     if (own.y == 1 && p.P == 0) return;  // written by the CTA that had the whole group
-    auto ml_of = [&](int i) {
-        return i < own.y ? p.ws.ml[(size_t)(own.x + i) * p.R + r]
-                         : p.ws.pre_ml[((size_t)kvh * p.pre_splits + (i - own.y)) * M + mrow];
-    };
-    auto o_of = [&](int i) {
-        return i < own.y ? p.ws.o + ((size_t)(own.x + i) * p.R + r) * D
-                         : p.ws.pre_o + (((size_t)kvh * p.pre_splits + (i - own.y)) * M + mrow) * D;
-    };
-    constexpr int kE = D / 32;  // columns a lane holds
-    float acc[kE] = {}, L = 0.f, top = kNone;
-    for (int base = warp; base < n; base += 32 * kCaWarps) {  // states base + 4k
-        const int mine = base + kCaWarps * lane;
-        float2 ml = make_float2(kNone, 0.f);
-        if (mine < n) ml = ml_of(mine);
-        const float was = top;
-        top = fmaxf(top, warp_max(ml.x));
-        const float f = exp2f(fmaxf(ml.x, kNone) - top), fo = exp2f(was - top);
-        L = L * fo + ml.y * f;
+    const RowSum<D> s = sum_states<D>(p, b, kvh, r, own.x, own.y, warp, kCaWarps, lane);
+    constexpr int kE = RowSum<D>::kE;
 #pragma unroll
-        for (int e = 0; e < kE; ++e) acc[e] *= fo;
-        const int cnt = min(32, (n - base + kCaWarps - 1) / kCaWarps);
-        for (int k0 = 0; k0 < cnt; k0 += 8) {
-            float x[8][kE];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const float* o = o_of(base + kCaWarps * min(k0 + k, cnt - 1)) + kE * lane;
-                if constexpr (kE == 4) {
-                    const float4 y = *reinterpret_cast<const float4*>(o);
-                    x[k][0] = y.x, x[k][1] = y.y, x[k][2] = y.z, x[k][3] = y.w;
-                } else {
-                    const float2 y = *reinterpret_cast<const float2*>(o);
-                    x[k][0] = y.x, x[k][1] = y.y;
-                }
-            }
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const float fk = __shfl_sync(0xffffffffu, f, min(k0 + k, 31));
-                if (k0 + k < cnt) {
-#pragma unroll
-                    for (int e = 0; e < kE; ++e) acc[e] = fmaf(x[k][e], fk, acc[e]);
-                }
-            }
-        }
-    }
-    L = warp_sum(L);
-#pragma unroll
-    for (int e = 0; e < kE; ++e) so[warp][kE * lane + e] = acc[e];
+    for (int e = 0; e < kE; ++e) so[warp][kE * lane + e] = s.acc[e];
     if (lane == 0) {
-        sl[warp] = L;
-        sm[warp] = top;
+        sl[warp] = s.L;
+        sm[warp] = s.top;
     }
     __syncthreads();
-    float mx = sm[0], f[kCaWarps];
+    float mx = sm[0], f[kCaWarps], L = 0.f;
 #pragma unroll
     for (int k = 1; k < kCaWarps; ++k) mx = fmaxf(mx, sm[k]);
-    L = 0.f;
 #pragma unroll
     for (int k = 0; k < kCaWarps; ++k) {
         f[k] = exp2f(sm[k] - mx);
