@@ -124,43 +124,32 @@ SD_DEVINL void mma16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint3
 }
 
 SD_DEVINL uint4 ld_row16(const uint8_t* p) { return __ldg(reinterpret_cast<const uint4*>(p)); }
-SD_DEVINL uint2 ld_row8(const uint8_t* p) { return __ldg(reinterpret_cast<const uint2*>(p)); }
 
-SD_DEVINL void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
-
-// What a lane holds of a step's 16 rows.
+// A step's 16 rows of K and V in shared memory: 16-byte chunk c of row r of either lies at r * kRow
+// + ((c ^ swizzle(r)) << 4), K first, then the rows' scales (K, V) and positions.
 template <int KIND, int D>
-struct Rows {
+struct Step {
     static constexpr int kEs = KIND == kBf16 ? 2 : 1;
     static constexpr int kRow = D * kEs;      // bytes of a row
-    static constexpr int kKc = kRow / 64;     // 16-byte pieces of a K row a lane holds
-    static constexpr int kVw = kRow / 32;     // 32-bit words of a V row a lane holds
-    uint4 k[2][kKc];       // K rows g8 and g8 + 8, bytes 64c + 16 t4 ..
-    float ks[2], vs[2];    // scales of rows g8 and g8 + 8
-    int pos[2];            // selected rows: their positions (INT_MAX: not attended by any query)
-    uint32_t v[4][kVw];    // V rows 2 t4, 2 t4 + 1, 2 t4 + 8, 2 t4 + 9, columns g8 * D/8 ..
-
-    SD_DEVINL void load_k(int h, const uint8_t* p) {  // p: the row's byte 16 t4
-#pragma unroll
-        for (int c = 0; c < kKc; ++c) k[h][c] = ld_row16(p + 64 * c);
-    }
-    SD_DEVINL void load_v(int r, const uint8_t* p) {  // p: the row's column g8 * D/8
-        if constexpr (kVw == 2) {
-            const uint2 w = ld_row8(p);
-            v[r][0] = w.x;
-            v[r][1] = w.y;
-        } else {
-#pragma unroll
-            for (int c = 0; c < kVw / 4; ++c) {
-                const uint4 w = ld_row16(p + 16 * c);
-                v[r][4 * c] = w.x;
-                v[r][4 * c + 1] = w.y;
-                v[r][4 * c + 2] = w.z;
-                v[r][4 * c + 3] = w.w;
-            }
-        }
-    }
+    static constexpr int kChunks = kRow / 16;
+    static constexpr int kKc = kRow / 64;     // 16-byte pieces of a K row a lane takes
+    static constexpr int kVw = kRow / 32;     // 32-bit words of a V row a lane takes
+    static constexpr int oV = 16 * kRow;
+    static constexpr int oKs = 2 * oV;
+    static constexpr int oVs = oKs + 64;
+    static constexpr int oPos = oVs + 64;
+    static constexpr int kBytes = oPos + 64;
+    SD_DEVINL static int swizzle(int r) { return kChunks == 4 ? (r >> 1) & 3 : r & 7; }
+    SD_DEVINL static int at(int r, int c) { return r * kRow + ((c ^ swizzle(r)) << 4); }
 };
+
+// The row (and row + 8) that stands at index i of the tensor cores' 8-row groups: with this order the
+// lanes that read shared memory together, rows perm(2j), perm(2j + 1) of K and perm(0), perm(2), ..
+// of V, are in different banks (128-byte rows; the order of keys does not matter otherwise).
+SD_DEVINL int perm(int i) {
+    constexpr uint32_t kPerm = 0x37156240u;  // 0 4 2 6 5 1 7 3
+    return (int)((kPerm >> (4 * i)) & 7u);
+}
 
 // ------------------------------------------------------------------ a warp's state
 
@@ -221,18 +210,20 @@ struct Queries {
     }
 };
 
-// S^T = K Q^T of a step: s[nq][2h + e] of row g8 + 8h and query 8nq + 2t4 + e.
+// S^T = K Q^T of the step at `st`: s[nq][2h + e] of row perm(g8) + 8h and query 8nq + 2t4 + e.
 template <int KIND, int D, int NQ>
-SD_DEVINL void ca_scores(const Rows<KIND, D>& rw, const Queries<D, NQ>& q, int lane, float (&s)[NQ][4]) {
+SD_DEVINL void ca_scores(const uint8_t* st, const Queries<D, NQ>& q, int lane, float (&s)[NQ][4]) {
     constexpr bool F16 = KIND != kBf16;
+    using S = Step<KIND, D>;
+    const int row = perm(lane >> 2), t4 = lane & 3;
 #pragma unroll
     for (int nq = 0; nq < NQ; ++nq)
 #pragma unroll
         for (int e = 0; e < 4; ++e) s[nq][e] = 0.f;
 #pragma unroll
-    for (int c = 0; c < Rows<KIND, D>::kKc; ++c) {
-        const uint32_t w0[4] = {rw.k[0][c].x, rw.k[0][c].y, rw.k[0][c].z, rw.k[0][c].w};
-        const uint32_t w1[4] = {rw.k[1][c].x, rw.k[1][c].y, rw.k[1][c].z, rw.k[1][c].w};
+    for (int c = 0; c < S::kKc; ++c) {
+        const uint4 k0 = lds128(st + S::at(row, 4 * c + t4)), k1 = lds128(st + S::at(row, 4 * c + t4) + 8 * S::kRow);
+        const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
         if constexpr (F16) {
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) {
@@ -259,7 +250,7 @@ SD_DEVINL void ca_scores(const Rows<KIND, D>& rw, const Queries<D, NQ>& q, int l
 
 // The online softmax of a step: s becomes the weights of the V rows.  Unless every query sees all
 // rows of the step (all), those above a query's limit (sl[8nq + 2t4 + e]) take no part (pos: the
-// positions of rows g8, g8 + 8).
+// positions of rows perm(g8), perm(g8) + 8).
 template <int KIND, int D, int NQ>
 SD_DEVINL void ca_softmax(float (&s)[NQ][4], const float (&ks)[2], const float (&vs)[2], const int (&pos)[2], bool all,
                           const int* sl, int t4, const Queries<D, NQ>& q, CaState<D, NQ>& st) {
@@ -336,9 +327,10 @@ SD_DEVINL void ca_softmax(float (&s)[NQ][4], const float (&ks)[2], const float (
         }
 }
 
-// O^T += V^T P^T of a step, P in s.
+// O^T += V^T P^T of the step at `at`, P in s.
 template <int KIND, int D, int NQ, bool HILO>
-SD_DEVINL void ca_output(const Rows<KIND, D>& rw, const float (&s)[NQ][4], CaState<D, NQ>& st) {
+SD_DEVINL void ca_output(const uint8_t* at, int lane, const float (&s)[NQ][4], CaState<D, NQ>& st) {
+    using S = Step<KIND, D>;
     constexpr bool F16 = KIND != kBf16;
     uint32_t ph[NQ][2], pl[NQ][2];
 #pragma unroll
@@ -358,9 +350,12 @@ SD_DEVINL void ca_output(const Rows<KIND, D>& rw, const float (&s)[NQ][4], CaSta
 #pragma unroll
         for (int nq = 0; nq < NQ; ++nq) mma16<F16>(st.o[md][nq], a0, a1, a2, a3, ph[nq][0], ph[nq][1]);
     };
-#pragma unroll
-    for (int w = 0; w < Rows<KIND, D>::kVw; ++w) {
-        const uint32_t A = rw.v[0][w], B = rw.v[1][w], C = rw.v[2][w], E = rw.v[3][w];
+    // columns g8 * D/8 .. of the rows that stand at indexes 2 t4, 2 t4 + 1 and 8 further on
+    const int g8 = lane >> 2, r0 = perm(2 * (lane & 3)), r1 = perm(2 * (lane & 3) + 1);
+    auto words = [&](int r, int w4) {  // words 4 w4 .. of row r
+        return lds128(at + S::oV + S::at(r, g8 * S::kVw / 4 + w4));
+    };
+    auto four = [&](int w, uint32_t A, uint32_t B, uint32_t C, uint32_t E) {
         if constexpr (F16) {
             const uint32_t l01 = biased<KIND>(__byte_perm(A, B, 0x5140)), l23 = biased<KIND>(__byte_perm(A, B, 0x7362));
             const uint32_t h01 = biased<KIND>(__byte_perm(C, E, 0x5140)), h23 = biased<KIND>(__byte_perm(C, E, 0x7362));
@@ -370,6 +365,23 @@ SD_DEVINL void ca_output(const Rows<KIND, D>& rw, const float (&s)[NQ][4], CaSta
         } else {
             pv(w, __byte_perm(A, B, 0x5410), __byte_perm(A, B, 0x7632), __byte_perm(C, E, 0x5410),
                __byte_perm(C, E, 0x7632));
+        }
+    };
+    if constexpr (S::kVw == 2) {  // half a chunk
+        const uint8_t* p0 = at + S::oV + S::at(r0, g8 >> 1) + 8 * (g8 & 1);
+        const uint8_t* p1 = at + S::oV + S::at(r1, g8 >> 1) + 8 * (g8 & 1);
+        const uint2 A = *reinterpret_cast<const uint2*>(p0), B = *reinterpret_cast<const uint2*>(p1);
+        const uint2 C = *reinterpret_cast<const uint2*>(p0 + 8 * S::kRow), E = *reinterpret_cast<const uint2*>(p1 + 8 * S::kRow);
+        four(0, A.x, B.x, C.x, E.x);
+        four(1, A.y, B.y, C.y, E.y);
+    } else {
+#pragma unroll
+        for (int w4 = 0; w4 < S::kVw / 4; ++w4) {
+            const uint4 A = words(r0, w4), B = words(r1, w4), C = words(r0 + 8, w4), E = words(r1 + 8, w4);
+            four(4 * w4, A.x, B.x, C.x, E.x);
+            four(4 * w4 + 1, A.y, B.y, C.y, E.y);
+            four(4 * w4 + 2, A.z, B.z, C.z, E.z);
+            four(4 * w4 + 3, A.w, B.w, C.w, E.w);
         }
     }
 }
@@ -465,35 +477,45 @@ SD_DEVINL RowSum<D> sum_states(const CaParams& p, int b, int kvh, int r, int fir
     return s;
 }
 
-template <int D, int NQ>
+// TS warps make a team that shares the steps it takes (all its warps see the same rows, each for 8 NQ of
+// the query rows); a team has a ring of stages of its own.
+template <int KIND, int D, int NQ, int TS>
 struct CaShared {
+    static constexpr int kStages = KIND == kBf16 && D == 128 ? 2 : 3;
     // a state row: column g8 * D/8 + 2md + j at 18 md + 2 g8 + j
     static constexpr int kPitch = D / 16 * 18;
-    float o[kCaWarps][8 * NQ][kPitch];
+    alignas(128) uint8_t ring[kCaWarps / TS][kStages][Step<KIND, D>::kBytes];
+    alignas(16) float o[kCaWarps][8 * NQ][kPitch];
     float2 ml[kCaWarps][8 * NQ];
-    uint2 q[NQ >= 2 ? D / 16 * NQ * 32 : 1];
-    float qs[8 * NQ];
-    int lim[8 * NQ];
+    uint2 q[NQ >= 2 ? TS * D / 16 * NQ * 32 : 1];
+    float qs[8 * NQ * TS];
+    int lim[8 * NQ * TS];
     unsigned part[kCaWarps], base;
     int b;
 };
 
 constexpr int kFoldSteps = 32;  // steps after which SD_F32 output folds the accumulators
 
-template <int KIND, int D, int NQ, bool HILO, bool SEL, int MINB>
+template <int KIND, int D, int NQ, int TS, bool HILO, bool SEL, int MINB>
 __global__ void __launch_bounds__(kCaThreads, MINB) cache_attend_kernel(const CaParams p) {
     constexpr bool F16 = KIND != kBf16;
-    constexpr int kRow = Rows<KIND, D>::kRow;
+    using S = Step<KIND, D>;
+    constexpr int kRow = S::kRow;
     constexpr int kMd = D / 16;
-    extern __shared__ uint4 ca_smem[];
-    auto& sh = *reinterpret_cast<CaShared<D, NQ>*>(ca_smem);
+    constexpr int kTeams = kCaWarps / TS;
+    using Shared = CaShared<KIND, D, NQ, TS>;
+    constexpr int kStages = Shared::kStages;
+    extern __shared__ __align__(128) uint8_t ca_smem[];
+    auto& sh = *reinterpret_cast<Shared*>(ca_smem);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g8 = lane >> 2, t4 = lane & 3;
+    const int team = warp / TS, half = warp % TS;  // half: which 8 NQ of the query rows
     const unsigned c = blockIdx.x;
     // The cache, qpos and q may be the preceding kernels' results.  Behind a prefix kernel of the same
     // call, which lets this one start only after its own wait for them, they are there already: the
     // wait is then for that kernel alone, and comes before its states are read.
     if (p.P == 0) pdl_wait();
-    pdl_launch_dependents();
+    // (No early trigger for the merge kernel, nor in that one for the next call's: CTAs that wait on an SM
+    // keep others from it.  8 ragged e4m3 caches called back to back: 71 us with both, 61 without.)
 
     // this CTA's run of units: [w0, w1) of all groups' units in order; no run is empty, so a
     // group's runs are in consecutive slots
@@ -585,105 +607,76 @@ __global__ void __launch_bounds__(kCaThreads, MINB) cache_attend_kernel(const Ca
         const uint8_t* vbase = p.vc + (size_t)g * p.T * kRow;
         const float* ksb = p.ks + (size_t)g * p.T;
         const float* vsb = p.vs + (size_t)g * p.T;
-        // lane l < 16 (and l + 16) resolves list row l of a step (SEL): its position, or -1 (an empty
-        // slot, an index outside the cache, a row no query sees)
+        const int nsteps = (j1 - j0 + 15) / 16;
+        // lane l < 16 (and l + 16) resolves row l of a step: its position, or -1 (past the run's rows, an
+        // empty slot, an index outside the cache, a row no query sees)
         auto resolve = [&](int step) {
-            int t = -1;
             const int i = j0 + 16 * step + (lane & 15);
+            int t = -1;
             if (i < j1) {
-                const int e = (int)((unsigned)i / (unsigned)p.block);
-                const long sel = p.idx[(size_t)g * p.n_idx + e];
-                const long pos = sel * p.block + (i - e * p.block);
-                if (sel != -1) {
-                    if (sel < 0 || pos >= p.T)
-                        report(p.err, SD_DEVERR_INDEX);
-                    else if (pos < len)
-                        t = (int)pos;
+                if constexpr (SEL) {
+                    const int e = (int)((unsigned)i / (unsigned)p.block);
+                    const long sel = p.idx[(size_t)g * p.n_idx + e];
+                    const long pos = sel * p.block + (i - e * p.block);
+                    if (sel != -1) {
+                        if (sel < 0 || pos >= p.T)
+                            report(p.err, SD_DEVERR_INDEX);
+                        else if (pos < len)
+                            t = (int)pos;
+                    }
+                } else {
+                    t = i;
                 }
             }
             return t;
         };
-        // row i of a step as a position to read: always one that a query sees
-        auto row_at = [&](int step, int rows, int i) {
-            if constexpr (SEL) return max(__shfl_sync(0xffffffffu, rows, i), 0);
-            return min(j0 + 16 * step + i, len - 1);
-        };
-        Rows<KIND, D> rw;
-        auto fetch_k = [&](int step, int rows) {
-            if (!SEL && j0 + 16 * step + 16 <= len) {
-                const int t = j0 + 16 * step + g8;
-                const uint8_t* kp = kbase + (size_t)t * kRow + 16 * t4;
-                rw.load_k(0, kp);
-                rw.load_k(1, kp + 8 * kRow);
-                if constexpr (F16) {
-                    rw.ks[0] = __ldg(ksb + t), rw.ks[1] = __ldg(ksb + t + 8);
-                    rw.vs[0] = __ldg(vsb + t), rw.vs[1] = __ldg(vsb + t + 8);
-                }
-            } else {
+        // Copies the team's rows of a step (resolved in `rows`) into a stage of its ring, a row that is none
+        // as row 0, which some query sees.  A team of two shares the copies: K, V.
+        auto fetch = [&](int stage, int rows) {
+            uint8_t* st = sh.ring[team][stage];
+            constexpr int kPer = 32 / S::kChunks > 0 ? 32 / S::kChunks : 1;  // rows an instruction copies
+            const int c0 = lane % S::kChunks, r0 = lane / S::kChunks;
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    if constexpr (SEL) {
-                        const int t0 = __shfl_sync(0xffffffffu, rows, g8 + 8 * h);
-                        rw.pos[h] = t0 < 0 ? 0x7fffffff : t0;
-                    }
-                    const int t = row_at(step, rows, g8 + 8 * h);
-                    rw.load_k(h, kbase + (size_t)t * kRow + 16 * t4);
-                    if constexpr (F16) {
-                        rw.ks[h] = __ldg(ksb + t);
-                        rw.vs[h] = __ldg(vsb + t);
-                    }
-                }
+            for (int r = 0; r < 16; r += kPer) {
+                const int t = max(__shfl_sync(0xffffffffu, rows, r + r0), 0);
+                const size_t off = (size_t)t * kRow + 16 * c0;
+                const int to = S::at(r + r0, c0);
+                if (TS == 1 || half == 0) cp_async16(st + to, kbase + off);
+                if (TS == 1 || half == 1) cp_async16(st + S::oV + to, vbase + off);
+            }
+            if (half == 0) {
+                if constexpr (F16) cp_async4(st + S::oKs + 4 * lane, (lane < 16 ? ksb : vsb) + max(rows, 0));
+                if (lane < 16) reinterpret_cast<int*>(st + S::oPos)[lane] = rows < 0 ? 0x7fffffff : rows;
             }
         };
-        auto fetch_v = [&](int step, int rows) {
-            if (!SEL && j0 + 16 * step + 16 <= len) {
-                const uint8_t* vp = vbase + (size_t)(j0 + 16 * step + 2 * t4) * kRow + g8 * (kRow / 8);
-                rw.load_v(0, vp);
-                rw.load_v(1, vp + kRow);
-                rw.load_v(2, vp + 8 * kRow);
-                rw.load_v(3, vp + 9 * kRow);
-            } else {
+        auto team_sync = [&]() {
+            if constexpr (TS == 1)
+                __syncwarp();
+            else
+                asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "n"(32 * TS) : "memory");
+        };
+        // the first steps' rows are on their way while the queries are prepared
+        int rows = resolve(team);
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int t = row_at(step, rows, 2 * t4 + (r & 1) + 8 * (r >> 1));
-                    rw.load_v(r, vbase + (size_t)t * kRow + g8 * (kRow / 8));
-                }
-            }
-        };
-        // asks L2 for the rows of a step (lane l: K row l, lane 16 + l: V row l) and their scales
-        auto ahead = [&](int step, int rows) {
-            const int i = j0 + 16 * step + (lane & 15);
-            const int t = SEL ? rows : i;
-            if (SEL ? t < 0 : i >= j1) return;
-            const uint8_t* at = (lane < 16 ? kbase : vbase) + (size_t)t * kRow;
-            prefetch_l2(at);
-            if constexpr (kRow > 128) prefetch_l2(at + 128);
-            if constexpr (F16) {
-                if (SEL || (lane & 15) == 0) prefetch_l2((lane < 16 ? ksb : vsb) + t);
-            }
-        };
-
-        const int nsteps = (j1 - j0 + 15) / 16;
-        int rows = -1, next = -1;
-        if constexpr (SEL) {
-            next = resolve(warp);
-            ahead(warp, next);
-        } else {
-            ahead(warp, 0);
-            ahead(warp + kCaWarps, 0);
+        for (int i = 0; i + 1 < kStages; ++i) {
+            if (team + i * kTeams < nsteps) fetch(i, rows);
+            cp_async_commit();
+            rows = resolve(team + (i + 1) * kTeams);
         }
 
         // the query rows 8nq + g8 as B fragments, their limits and the smallest limit
         Queries<D, NQ> q;
-        q.sh = sh.q;
+        q.sh = sh.q + half * (kMd * NQ * 32);
+        const int* lim = sh.lim + half * 8 * NQ;
         __syncthreads();  // (the segment before is done with the limits and the states)
         int lmin = p.T;  // rows every query sees
-        if (tid < 8 * NQ) sh.lim[tid] = tid < p.R ? min(p.qpos[(size_t)b * p.V + tid / p.G], p.T - 1) : -1;
+        if (tid < 8 * NQ * TS) sh.lim[tid] = tid < p.R ? min(p.qpos[(size_t)b * p.V + tid / p.G], p.T - 1) : -1;
         for (int v = 0; v < p.V; ++v) lmin = min(lmin, p.qpos[(size_t)b * p.V + v] + 1);
 #pragma unroll
-        for (int nq = 0; nq < NQ; ++nq) {
-            if (Queries<D, NQ>::kShared && warp != nq) continue;  // tile nq is warp nq's to prepare
-            const int r = 8 * nq + g8;
+        for (int nt = 0; nt < (Queries<D, NQ>::kShared ? TS * NQ : NQ); ++nt) {
+            if (Queries<D, NQ>::kShared && warp != nt) continue;  // tile nt is warp nt's to prepare
+            const int nq = Queries<D, NQ>::kShared ? 0 : nt;
+            const int r = 8 * nt + g8;
             const bool have = r < p.R;
             const int v = have ? r / p.G : 0, gi = have ? r - v * p.G : 0;
             const uint8_t* qrow = p.q + (((size_t)b * p.V + v) * p.Hq + (size_t)kvh * p.G + gi) * (D * 2);
@@ -691,7 +684,7 @@ __global__ void __launch_bounds__(kCaThreads, MINB) cache_attend_kernel(const Ca
             if constexpr (F16) {
                 uint32_t top = 0u;
 #pragma unroll
-                for (int cc = 0; cc < Rows<KIND, D>::kKc; ++cc)
+                for (int cc = 0; cc < S::kKc; ++cc)
 #pragma unroll
                     for (int hh = 0; hh < 2; ++hh) {  // dims 64 cc + 16 t4 + 8 hh ..
                         const uint4 x = have ? ld_row16(qrow + 2 * (64 * cc + 16 * t4 + 8 * hh)) : make_uint4(0u, 0u, 0u, 0u);
@@ -716,7 +709,7 @@ __global__ void __launch_bounds__(kCaThreads, MINB) cache_attend_kernel(const Ca
                 if (t4 == 0) sh.qs[r] = up * p.scale_log2;
             } else {
 #pragma unroll
-                for (int cc = 0; cc < Rows<KIND, D>::kKc; ++cc) {  // dims 32 cc + 8 t4 ..
+                for (int cc = 0; cc < S::kKc; ++cc) {  // dims 32 cc + 8 t4 ..
                     const uint4 x = have ? ld_row16(qrow + 2 * (32 * cc + 8 * t4)) : make_uint4(0u, 0u, 0u, 0u);
                     raw[2 * cc][0] = x.x;
                     raw[2 * cc][1] = x.y;
@@ -728,7 +721,7 @@ __global__ void __launch_bounds__(kCaThreads, MINB) cache_attend_kernel(const Ca
 #pragma unroll
             for (int k = 0; k < kMd; ++k) {
                 if constexpr (Queries<D, NQ>::kShared) {
-                    sh.q[(k * NQ + nq) * 32 + lane] = make_uint2(raw[k][0], raw[k][1]);
+                    sh.q[((nt / NQ * kMd + k) * NQ + nt % NQ) * 32 + lane] = make_uint2(raw[k][0], raw[k][1]);
                 } else {
                     q.f[k][nq][0] = raw[k][0];
                     q.f[k][nq][1] = raw[k][1];
@@ -738,7 +731,7 @@ __global__ void __launch_bounds__(kCaThreads, MINB) cache_attend_kernel(const Ca
         __syncthreads();
 #pragma unroll
         for (int nq = 0; nq < NQ; ++nq) {
-            const float2 f = *reinterpret_cast<const float2*>(&sh.qs[8 * nq + 2 * t4]);
+            const float2 f = *reinterpret_cast<const float2*>(&sh.qs[8 * (half * NQ + nq) + 2 * t4]);
             q.qs[nq][0] = f.x;
             q.qs[nq][1] = f.y;
         }
@@ -785,61 +778,55 @@ __global__ void __launch_bounds__(kCaThreads, MINB) cache_attend_kernel(const Ca
             st.clear();
         };
 
-        // Pass s computes step s and fetches step s + 4, K rows as soon as the scores have used the last
-        // ones and V rows after the output (the first pass, s = warp - 4, only fetches).
         bool first = true;
-        int since = 0;
-        for (int s = warp - kCaWarps; s < nsteps; s += kCaWarps) {
-            const bool work = s >= 0, more = s + kCaWarps < nsteps;
-            if constexpr (SEL) {
-                rows = next;
-                next = resolve(s + 2 * kCaWarps);
-                ahead(s + 2 * kCaWarps, next);
-            } else {
-                ahead(s + 3 * kCaWarps, 0);
-            }
-            float sc[NQ][4], ks[2], vs[2];
-            int pos[2];
-            bool all = true;
-            if (work) {
-                ca_scores<KIND, D, NQ>(rw, q, lane, sc);
-                if constexpr (SEL) {
-                    pos[0] = rw.pos[0], pos[1] = rw.pos[1];
-                    all = __all_sync(0xffffffffu, max(pos[0], pos[1]) < lmin);
-                } else {
-                    pos[0] = j0 + 16 * s + g8;
-                    pos[1] = pos[0] + 8;
-                    all = j0 + 16 * s + 16 <= lmin;
-                }
+        int since = 0, stage = 0;
+        for (int n = team; n < nsteps || first; n += kTeams) {
+            if (n < nsteps) {
+                // this step has landed for every warp of the team, and all are done with the stage of the one before,
+                // which takes the rows kStages - 1 steps ahead
+                cp_async_wait<kStages - 2>();
+                team_sync();
+                if (n + (kStages - 1) * kTeams < nsteps) fetch(stage == 0 ? kStages - 1 : stage - 1, rows);
+                cp_async_commit();
+                rows = resolve(n + kStages * kTeams);
+                const uint8_t* at = sh.ring[team][stage];
+                const int row = perm(g8);
+                float sc[NQ][4], ks[2], vs[2];
+                int pos[2];
+                ca_scores<KIND, D, NQ>(at, q, lane, sc);
 #pragma unroll
-                for (int h = 0; h < 2; ++h) ks[h] = rw.ks[h], vs[h] = rw.vs[h];
+                for (int h = 0; h < 2; ++h) {
+                    pos[h] = reinterpret_cast<const int*>(at + S::oPos)[row + 8 * h];
+                    ks[h] = reinterpret_cast<const float*>(at + S::oKs)[row + 8 * h];
+                    vs[h] = reinterpret_cast<const float*>(at + S::oVs)[row + 8 * h];
+                }
+                const bool all = SEL ? __all_sync(0xffffffffu, max(pos[0], pos[1]) < lmin) : j0 + 16 * n + 16 <= lmin;
+                ca_softmax<KIND, D, NQ>(sc, ks, vs, pos, all, lim, t4, q, st);
+                ca_output<KIND, D, NQ, HILO>(at, lane, sc, st);
+                stage = stage == kStages - 1 ? 0 : stage + 1;
             }
-            if (more) fetch_k(s + kCaWarps, rows);
-            if (work) {
-                ca_softmax<KIND, D, NQ>(sc, ks, vs, pos, all, sh.lim, t4, q, st);
-                ca_output<KIND, D, NQ, HILO>(rw, sc, st);
-            }
-            if (more) fetch_v(s + kCaWarps, rows);
-            if (!more || (HILO && ++since > kFoldSteps)) {
+            if (n + kTeams >= nsteps || (HILO && ++since == kFoldSteps)) {
                 fold(first);
                 first = false;
-                since = 1;
+                since = 0;
             }
         }
+        cp_async_wait<0>();
         __syncthreads();
         const bool whole = j == 0u && seg == tb && p.P == 0;
         const size_t slot = (size_t)c + g;
         for (int i = tid; i < p.R * (D / 2); i += kCaThreads) {
             const int r = i / (D / 2), d = 2 * (i - r * (D / 2));
             const int gg = d / (D / 8), at = 18 * ((d - gg * (D / 8)) / 2) + 2 * gg;
-            float M = sh.ml[0][r].x;
+            const int hf = r / (8 * NQ), rr = r - hf * 8 * NQ;  // warps hf, hf + TS, .. hold this row
+            float M = sh.ml[hf][rr].x;
 #pragma unroll
-            for (int k = 1; k < kCaWarps; ++k) M = fmaxf(M, sh.ml[k][r].x);
+            for (int k = 1; k < kTeams; ++k) M = fmaxf(M, sh.ml[hf + k * TS][rr].x);
             float L = 0.f, x = 0.f, y = 0.f;
 #pragma unroll
-            for (int k = 0; k < kCaWarps; ++k) {
-                const float2 ml = sh.ml[k][r];
-                const float2 o = *reinterpret_cast<const float2*>(&sh.o[k][r][at]);
+            for (int k = 0; k < kTeams; ++k) {
+                const float2 ml = sh.ml[hf + k * TS][rr];
+                const float2 o = *reinterpret_cast<const float2*>(&sh.o[hf + k * TS][rr][at]);
                 const float f = exp2f(ml.x - M);
                 L = fmaf(ml.y, f, L);
                 x = fmaf(o.x, f, x);
@@ -870,56 +857,69 @@ __global__ void __launch_bounds__(kCaThreads, MINB) cache_attend_kernel(const Ca
     if (p.P > 0) pdl_wait();
 }
 
-// One CTA a query row: every warp takes each fourth state, and the warps' sums meet in shared memory in
-// a fixed order.  (The last CTA of a group merging it instead of a second kernel was measured: it saves a
-// launch and loses more, since one CTA then does what 4 to 32 do here: 18.7 -> 22.4 us for the
-// selected blocks, 65 -> 77 us for 64 sequences behind a prefix of 32768.)
-template <int D>
+// The states of every query row into the output.  kSplit: one CTA a row, whose warps take each fourth state
+// and meet in shared memory in a fixed order; else one warp a row.  (The last CTA of a group merging
+// it instead of a second kernel was measured: it saves a launch and loses more, since one CTA then does
+// what 4 to 32 do here: 18.7 -> 22.4 us for the selected blocks, 65 -> 77 us for 64 sequences behind
+// a prefix of 32768.)
+template <int D, bool kSplit>
 __global__ void __launch_bounds__(kCaThreads) cache_merge_kernel(const CaParams p) {
-    __shared__ float so[kCaWarps][D];
-    __shared__ float sl[kCaWarps], sm[kCaWarps];
+    constexpr int kE = RowSum<D>::kE;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int h = (int)blockIdx.x, v = (int)blockIdx.y, b = (int)blockIdx.z;
-    const int kvh = h / p.G, gi = h - kvh * p.G, r = v * p.G + gi;
+    const unsigned row = kSplit ? blockIdx.x : blockIdx.x * kCaWarps + warp;  // (b, v, h)
+    const unsigned bv = row / (unsigned)p.Hq, h = row - bv * p.Hq;
+    const unsigned b = bv / (unsigned)p.V, v = bv - b * p.V;
+    const unsigned kvh = h / (unsigned)p.G;
+    const int r = (int)(v * p.G + h - kvh * p.G);
+    if (b >= (unsigned)p.B) return;
     pdl_wait();
-    pdl_launch_dependents();
     const int2 own = p.ws.meta[b * p.Hkv + kvh];
     if (own.y == 1 && p.P == 0) return;  // written by the CTA that had the whole group
-    const RowSum<D> s = sum_states<D>(p, b, kvh, r, own.x, own.y, warp, kCaWarps, lane);
-    constexpr int kE = RowSum<D>::kE;
+    if constexpr (kSplit) {
+        __shared__ float so[kCaWarps][D];
+        __shared__ float sl[kCaWarps], sm[kCaWarps];
+        const RowSum<D> s = sum_states<D>(p, (int)b, (int)kvh, r, own.x, own.y, warp, kCaWarps, lane);
 #pragma unroll
-    for (int e = 0; e < kE; ++e) so[warp][kE * lane + e] = s.acc[e];
-    if (lane == 0) {
-        sl[warp] = s.L;
-        sm[warp] = s.top;
-    }
-    __syncthreads();
-    float mx = sm[0], f[kCaWarps], L = 0.f;
+        for (int e = 0; e < kE; ++e) so[warp][kE * lane + e] = s.acc[e];
+        if (lane == 0) {
+            sl[warp] = s.L;
+            sm[warp] = s.top;
+        }
+        __syncthreads();
+        float mx = sm[0], f[kCaWarps], L = 0.f;
 #pragma unroll
-    for (int k = 1; k < kCaWarps; ++k) mx = fmaxf(mx, sm[k]);
-#pragma unroll
-    for (int k = 0; k < kCaWarps; ++k) {
-        f[k] = exp2f(sm[k] - mx);
-        L = fmaf(sl[k], f[k], L);
-    }
-    const float inv = L > 0.f ? 1.f / L : 0.f;
-    const size_t row = ((size_t)b * p.V + v) * p.Hq + h;
-    if (threadIdx.x < D / 2) {
-        const int d = 2 * (int)threadIdx.x;
-        float x = 0.f, y = 0.f;
+        for (int k = 1; k < kCaWarps; ++k) mx = fmaxf(mx, sm[k]);
 #pragma unroll
         for (int k = 0; k < kCaWarps; ++k) {
-            x = fmaf(so[k][d], f[k], x);
-            y = fmaf(so[k][d + 1], f[k], y);
+            f[k] = exp2f(sm[k] - mx);
+            L = fmaf(sl[k], f[k], L);
         }
-        store_pair(p.out, p.out_bf16 != 0, row * D + d, x * inv, y * inv);
+        const float inv = L > 0.f ? 1.f / L : 0.f;
+        if (threadIdx.x < D / 2) {
+            const int d = 2 * (int)threadIdx.x;
+            float x = 0.f, y = 0.f;
+#pragma unroll
+            for (int k = 0; k < kCaWarps; ++k) {
+                x = fmaf(so[k][d], f[k], x);
+                y = fmaf(so[k][d + 1], f[k], y);
+            }
+            store_pair(p.out, p.out_bf16 != 0, (size_t)row * D + d, x * inv, y * inv);
+        }
+        if (threadIdx.x == 0) p.lse[row] = L > 0.f ? (mx + log2f(L)) * 0.69314718055994530942f : -INFINITY;
+    } else {
+        const RowSum<D> s = sum_states<D>(p, (int)b, (int)kvh, r, own.x, own.y, 0, 1, lane);
+        const float inv = s.L > 0.f ? 1.f / s.L : 0.f;
+#pragma unroll
+        for (int e = 0; e < kE; e += 2)
+            store_pair(p.out, p.out_bf16 != 0, (size_t)row * D + kE * lane + e, s.acc[e] * inv, s.acc[e + 1] * inv);
+        if (lane == 0) p.lse[row] = s.L > 0.f ? (s.top + log2f(s.L)) * 0.69314718055994530942f : -INFINITY;
     }
-    if (threadIdx.x == 0) p.lse[row] = L > 0.f ? (mx + log2f(L)) * 0.69314718055994530942f : -INFINITY;
 }
 
-// CTAs an SM holds of a variant (its __launch_bounds__): what its registers allow without spills.
-constexpr int ca_ctas_per_sm(int kind, int d, int nq) {
-    return nq == 4 ? (d == 64 ? 3 : 2) : (kind == kBf16 && d == 128) || nq == 2 ? 3 : 4;
+// CTAs an SM holds of a variant (its __launch_bounds__): what its registers and rings allow.
+constexpr int ca_ctas_per_sm(int kind, int d, int nq, int ts) {
+    if (d == 64) return kind != kBf16 && nq == 1 ? 4 : 3;
+    return kind == kBf16 || (nq == 2 && ts == 1) ? 2 : 3;
 }
 
 int ca_kind(const sd_cache_attend_args* a) {
@@ -932,7 +932,7 @@ CaPlan ca_plan(const sd_cache_attend_args* a) {
     const int R = (a->Hq / a->Hkv) * a->V;
     const long rows = a->idx != nullptr ? (long)a->n_idx * a->block : a->T;
     const long units = NG * std::max<long>(1, (rows + kCaTile - 1) / kCaTile);
-    pl.ctas = (int)std::min<long>(units, (long)num_sms() * ca_ctas_per_sm(ca_kind(a), a->d, R <= 8 ? 1 : R <= 16 ? 2 : 4));
+    pl.ctas = (int)std::min<long>(units, (long)num_sms() * ca_ctas_per_sm(ca_kind(a), a->d, R <= 8 ? 1 : 2, R <= 16 ? 1 : 2));
     pl.slots = (int)(pl.ctas + NG - 1);
     pl.pre_splits = a->P > 0 ? prefix_splits(a) : 0;
     return pl;
@@ -973,12 +973,13 @@ sd_status ca_validate(const sd_cache_attend_args* a, bool pointers) {
     return SD_OK;
 }
 
-template <int KIND, int D, int NQ, bool HILO>
+template <int KIND, int D, int NQ, int TS, bool HILO>
 sd_status ca_launch(const CaParams& p, const CaPlan& pl, cudaStream_t st) {
-    constexpr int kMinB = ca_ctas_per_sm(KIND, D, NQ);
-    constexpr int kBytes = (int)sizeof(CaShared<D, NQ>);
-    auto kern = p.idx != nullptr ? cache_attend_kernel<KIND, D, NQ, HILO, true, kMinB>
-                                 : cache_attend_kernel<KIND, D, NQ, HILO, false, kMinB>;
+    constexpr int kMinB = ca_ctas_per_sm(KIND, D, NQ, TS);
+    constexpr int kBytes = (int)sizeof(CaShared<KIND, D, NQ, TS>);
+    static_assert(kMinB * (kBytes + 1024) <= 227 * 1024, "the CTAs of an SM share its memory");
+    auto kern = p.idx != nullptr ? cache_attend_kernel<KIND, D, NQ, TS, HILO, true, kMinB>
+                                 : cache_attend_kernel<KIND, D, NQ, TS, HILO, false, kMinB>;
     if (kBytes > 48 * 1024)
         SD_CUDA_CHECK(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes),
                       "sd_cache_attend: cudaFuncSetAttribute");
@@ -989,9 +990,9 @@ sd_status ca_launch(const CaParams& p, const CaPlan& pl, cudaStream_t st) {
 
 template <int KIND, int D, bool HILO>
 sd_status ca_dispatch_rows(const CaParams& p, const CaPlan& pl, cudaStream_t st) {
-    return p.R <= 8    ? ca_launch<KIND, D, 1, HILO>(p, pl, st)
-           : p.R <= 16 ? ca_launch<KIND, D, 2, HILO>(p, pl, st)
-                       : ca_launch<KIND, D, 4, HILO>(p, pl, st);
+    return p.R <= 8    ? ca_launch<KIND, D, 1, 1, HILO>(p, pl, st)
+           : p.R <= 16 ? ca_launch<KIND, D, 2, 1, HILO>(p, pl, st)
+                       : ca_launch<KIND, D, 2, 2, HILO>(p, pl, st);
 }
 template <int KIND, int D>
 sd_status ca_dispatch(const CaParams& p, const CaPlan& pl, cudaStream_t st) {
@@ -1058,8 +1059,12 @@ extern "C" sd_status sd_cache_attend(const sd_cache_attend_args* a, void* stream
         default: st = d128 ? ca_dispatch<kBf16, 128>(p, pl, cs) : ca_dispatch<kBf16, 64>(p, pl, cs); break;
     }
     if (st != SD_OK) return st;
-    const dim3 grid((unsigned)a->Hq, (unsigned)a->V, (unsigned)a->B);
-    SD_CUDA_CHECK(launch_pdl(d128 ? cache_merge_kernel<128> : cache_merge_kernel<64>, grid, dim3(kCaThreads), 0, cs, p),
+    // a CTA a row while that leaves the GPU room (its states are then read four at a time), else a warp
+    const unsigned rows = (unsigned)a->B * a->V * a->Hq;
+    const bool split = rows <= 8u * (unsigned)num_sms();
+    const auto merge = d128 ? (split ? cache_merge_kernel<128, true> : cache_merge_kernel<128, false>)
+                            : (split ? cache_merge_kernel<64, true> : cache_merge_kernel<64, false>);
+    SD_CUDA_CHECK(launch_pdl(merge, dim3(split ? rows : (rows + kCaWarps - 1) / kCaWarps), dim3(kCaThreads), 0, cs, p),
                   "sd_cache_attend: merge launch");
     return launch_status(who);
 }

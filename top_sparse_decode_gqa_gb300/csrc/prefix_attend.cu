@@ -13,11 +13,13 @@
 //
 // Bound: for up to about 256 rows a KV head HBM (a key tile is read once for both row tiles),
 // beyond it the tensor cores and the exponentials.  One CTA an SM; per key tile of 128 and row tile
-// t = 0, 1: S_t (128 x 128 fp32 accumulators in TMEM) by d/16 MMAs, softmax by warpgroup t (one
-// thread a row: no shuffles), P_t back into the TMEM columns S_t held (two bf16 parts of 64
-// columns each, or one), O_t += P_t V with P from TMEM and V as it lies in memory (MN-major).
-// The MMA warp alternates the tiles, so the tensor cores work on one while the other's softmax
-// runs.  O_t is rescaled only when a row's maximum has grown by more than 2^8 since the last time
+// t = 0, 1: S_t (128 x 128 fp32 accumulators in TMEM) by d/16 MMAs, softmax by two warpgroups (two
+// threads a row, 64 columns each: no shuffles, and one thread's chain of 128 exponentials was what the
+// tensor cores waited for; S is read twice, 32 columns at a time, which leaves the 16 warps 96
+// registers a thread), P_t back into the TMEM columns S_t held (32 keys: 16 columns of one
+// bf16 part, 16 of the other), O_t += P_t V with P from TMEM and V as it lies in memory
+// (MN-major).  The MMA warp alternates the tiles, so the tensor cores work on one while the other's
+// softmax runs.  O_t is rescaled only when a row's maximum has grown by more than 2^8 since the last time
 // (weights stay below 2^8; the quotient O / l does not change), which is rare after the first tiles.
 // The tensor cores cut what they add to a sum (2^-24 of it), so SD_F32 output starts O_t anew every
 // 16 tiles and adds up in fp32 in the workspace (L2).  The softmax takes 4 to 5 instructions an
@@ -36,8 +38,9 @@ namespace {
 
 constexpr int kPfKeys = 128;  // keys a tile
 constexpr int kPfRows = 128;  // query rows a tile
-constexpr int kPfProd = 8, kPfMma = 9;  // warps 0-3 and 4-7: softmax of row tiles 0 and 1
-constexpr int kPfThreads = 32 * 10;
+// warps 0-7 and 8-15: softmax of row tiles 0 and 1 (warps 4-7 and 12-15 of keys 64-127)
+constexpr int kPfProd = 16, kPfMma = 17;
+constexpr int kPfThreads = 32 * 18;
 constexpr int kPfStages = 2;
 constexpr int kPfFold = 16;      // key tiles after which SD_F32 output folds O
 constexpr float kPfGrow = 8.f;  // the growth of a row's maximum (base 2) that O is rescaled at
@@ -52,7 +55,8 @@ struct PfLayout {
     static constexpr int oV = oK + kPfStages * kTile;
     static constexpr int oBars = oV + kPfStages * kTile;
     static constexpr int oMisc = oBars + 32 * 8;
-    static constexpr int kBytes = oMisc + 32 + 1024;  // slack for the 1024-byte alignment
+    static constexpr int oTop = oMisc + 32;           // [2][2][128] floats: the halves' maxima, then their sums
+    static constexpr int kBytes = oTop + 2048 + 1024;  // slack for the 1024-byte alignment
 };
 
 struct PfParams {
@@ -141,7 +145,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         }
         for (int t = 0; t < 2; ++t) {
             mbar_init(&sfull[t], 1);
-            mbar_init(&pfull[t], 4);  // one arrival a softmax warp
+            mbar_init(&pfull[t], 8);  // one arrival a softmax warp
             mbar_init(&ofull[t], 1);
         }
         mbar_init(drain, 1);
@@ -211,8 +215,9 @@ __global__ void __launch_bounds__(kPfThreads, 1)
 #pragma unroll
                 for (int k = 0; k < kPfKeys / 16; ++k) {
                     const uint64_t bd = umma_desc_mn_sw128(b0 + k * 2048, L::kAtom);
-                    umma_bf16_ta(o, a + 8 * k, bd, kIdO, (HILO ? n % kPfFold : n) > 0 || k > 0 ? 1u : 0u);
-                    if (HILO) umma_bf16_ta(o, a + 64 + 8 * k, bd, kIdO, 1u);
+                    const uint32_t ak = a + 32 * (k >> 1) + 8 * (k & 1);
+                    umma_bf16_ta(o, ak, bd, kIdO, (HILO ? n % kPfFold : n) > 0 || k > 0 ? 1u : 0u);
+                    if (HILO) umma_bf16_ta(o, ak + 16, bd, kIdO, 1u);
                 }
             };
             bool ok = pf_wait(qfull, 0u, abort_flag, lim) && pf_wait(&kfull[0], 0u, abort_flag, lim);
@@ -244,28 +249,43 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                 mbar_wait(drain, 0u, lim);
             }
         }
-    } else if ((warp >> 2) < nq) {
-        const int t = warp >> 2, quarter = warp & 3;
+    } else if (warp < kPfProd && (warp >> 3) < nq) {
+        const int t = warp >> 3, half = (warp >> 2) & 1, quarter = warp & 3;
+        constexpr int kCols = kPfKeys / 2, kOut = D / 2;  // columns of S and of O that this thread has
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
-        const uint32_t ts = tmem + lanes + t * 128, to = tmem + lanes + 256 + t * 128;
+        const uint32_t ts = tmem + lanes + t * 128 + half * kCols, to = tmem + lanes + 256 + t * 128 + half * kOut;
         const int r = quarter * 32 + lane;  // this thread's row of the tile
         const bool mine = r < p.G * p.bpt;
         const long row = (long)(2 * pair + t) * p.G * p.bpt + r;
         const bool store = mine && row < p.M;
         const size_t at = ((size_t)kvh * p.splits + split) * p.M + (store ? row : 0);
+        float* tops = reinterpret_cast<float*>(sm + L::oTop) + t * 256;
+        // a barrier of the tile's 256 softmax threads that tells whether any of them said yes
+        auto vote = [&](bool yes) {
+            int any;
+            asm volatile(
+                "{\n\t.reg .pred p, q;\n\t"
+                "setp.ne.s32 p, %1, 0;\n\t"
+                "barrier.cta.red.or.pred q, %2, 256, p;\n\t"
+                "selp.s32 %0, 1, 0, q;\n\t}"
+                : "=r"(any)
+                : "r"(yes ? 1 : 0), "r"(1 + t)
+                : "memory");
+            return any != 0;
+        };
         float m = -INFINITY, l = 0.f;
         float fm = 0.f;       // the maximum that the folded sums in the workspace are relative to
         bool folded = false;
-        // O_t of this row, added to what was folded before, to the workspace
+        // this thread's columns of O_t, added to what was folded before, to the workspace
         auto write_o = [&]() {
             const float f = folded ? fast_exp2(fm - m) : 0.f;
 #pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
+            for (int c = 0; c < kOut / 32; ++c) {
                 uint32_t o[32];
                 tmem_ld32_nowait(to + 32 * c, o);
                 tmem_wait_ld();
                 if (store) {
-                    float4* dst = reinterpret_cast<float4*>(p.o + at * D + 32 * c);
+                    float4* dst = reinterpret_cast<float4*>(p.o + at * D + half * kOut + 32 * c);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         float4 x = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
@@ -283,67 +303,78 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         };
         bool ok = true;
         for (int n = 0; n < nt; ++n) {
-            ok = __all_sync(0xffffffffu, pf_wait(&sfull[t], (uint32_t)n & 1u, abort_flag, lim));
-            if (!ok) break;
+            // every thread reaches the votes whatever its wait came to, so none waits in them for ever
+            ok = pf_wait(&sfull[t], (uint32_t)n & 1u, abort_flag, lim);
             tc_fence_after_sync();
             if (HILO && n > 0 && n % kPfFold == 0) write_o();
-            uint32_t s[128];
+            const int valid = p.P - (n0 + n) * kPfKeys - half * kCols;  // keys of this half within the prefix
+            // 32 columns of S, the keys past the prefix as -inf
+            auto load = [&](int c, uint32_t (&s)[32]) {
+                tmem_ld32_nowait(ts + 32 * c, s);
+                tmem_wait_ld();
+                if (valid < 32 * c + 32) {
 #pragma unroll
-            for (int c = 0; c < 4; ++c) tmem_ld32_nowait(ts + 32 * c, s + 32 * c);
-            tmem_wait_ld();
-            const int valid = p.P - (n0 + n) * kPfKeys;  // keys of the tile within the prefix
-            if (valid < kPfKeys) {
+                    for (int i = 0; i < 32; ++i)
+                        if (32 * c + i >= valid) s[i] = 0xff800000u;
+                }
+            };
+            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int i = 0; i < kPfKeys; ++i)
-                    if (i >= valid) s[i] = 0xff800000u;  // -inf
+            for (int c = 0; c < kCols / 32; ++c) {
+                uint32_t s[32];
+                load(c, s);
+#pragma unroll
+                for (int i = 0; i < 32; i += 2)
+                    mx[(i >> 1) & 3] = max3(mx[(i >> 1) & 3], __uint_as_float(s[i]), __uint_as_float(s[i + 1]));
             }
-            float mx[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                mx[j] = max3(__uint_as_float(s[3 * j]), __uint_as_float(s[3 * j + 1]), __uint_as_float(s[3 * j + 2]));
-#pragma unroll
-            for (int i = 12; i < kPfKeys; i += 2)
-                mx[(i >> 1) & 3] = max3(mx[(i >> 1) & 3], __uint_as_float(s[i]), __uint_as_float(s[i + 1]));
             const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
-            // (rows past the tile's query rows hold whatever shared memory held: left alone)
-            const float grown = mine && top > m + kPfGrow ? top : m;
-            if (n == 0) {
-                m = top;
-            } else if (__any_sync(0xffffffffu, grown != m)) {
-                const float f = fast_exp2(m - grown);
+            // (rows past the tile's query rows hold whatever shared memory held: they ask for nothing)
+            if (vote(n == 0 || (mine && top > m + kPfGrow) || !ok)) {
+                tops[half * 128 + r] = top;
+                if (vote(*abort_flag != 0)) {  // (the vote: all of the tile's threads leave, or none)
+                    ok = false;
+                    break;
+                }
+                const float both = fmaxf(top, tops[(half ^ 1) * 128 + r]);
+                const float grown = n == 0 || (mine && both > m + kPfGrow) ? both : m;
+                const float f = n == 0 ? 0.f : fast_exp2(m - grown);
                 l *= f;
                 m = grown;
+                if (n > 0) {
 #pragma unroll
-                for (int c = 0; c < D / 32; ++c) {
-                    uint32_t o[32];
-                    tmem_ld32_nowait(to + 32 * c, o);
-                    tmem_wait_ld();
+                    for (int c = 0; c < kOut / 32; ++c) {
+                        uint32_t o[32];
+                        tmem_ld32_nowait(to + 32 * c, o);
+                        tmem_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                    tmem_st16(to + 32 * c, o);
-                    tmem_st16(to + 32 * c + 16, o + 16);
+                        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                        tmem_st16(to + 32 * c, o);
+                        tmem_st16(to + 32 * c + 16, o + 16);
+                    }
                 }
+                vote(false);  // the maxima are read before the next ones are written
             }
             uint64_t sum[2] = {0ull, 0ull};
             const uint64_t c2 = pack2(p.scale_log2, p.scale_log2), m2 = pack2(-m, -m);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                uint32_t hi[16], lo[16];
+            for (int c = 0; c < kCols / 32; ++c) {
+                uint32_t s[32], hi[16], lo[16];
+                load(c, s);
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    const float2 z = unpack2(fma2(
-                        pack2(__uint_as_float(s[32 * c + 2 * i]), __uint_as_float(s[32 * c + 2 * i + 1])), c2, m2));
+                    const float2 z =
+                        unpack2(fma2(pack2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), c2, m2));
                     const float x = fast_exp2(z.x), y = fast_exp2(z.y);
                     const uint64_t xy = pack2(x, y);
                     sum[i & 1] = add2(sum[i & 1], xy);
                     hi[i] = pack_bf16x2(x, y);
                     if constexpr (HILO) {  // what is left of the weights: x - hi is exact
-                        const float2 r = unpack2(fma2(pack2(bf16lo(hi[i]), bf16hi(hi[i])), pack2(-1.f, -1.f), xy));
-                        lo[i] = pack_bf16x2(r.x, r.y);
+                        const float2 q = unpack2(fma2(pack2(bf16lo(hi[i]), bf16hi(hi[i])), pack2(-1.f, -1.f), xy));
+                        lo[i] = pack_bf16x2(q.x, q.y);
                     }
                 }
-                tmem_st16(ts + 16 * c, hi);
-                if constexpr (HILO) tmem_st16(ts + 64 + 16 * c, lo);
+                tmem_st16(ts + 32 * c, hi);
+                if constexpr (HILO) tmem_st16(ts + 32 * c + 16, lo);
             }
             const float2 s2 = unpack2(add2(sum[0], sum[1]));
             l += s2.x + s2.y;
@@ -352,11 +383,13 @@ __global__ void __launch_bounds__(kPfThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&pfull[t]);
         }
-        if (ok) ok = __all_sync(0xffffffffu, pf_wait(&ofull[t], 0u, abort_flag, lim));
-        if (ok) {
+        // (a tile's threads leave the loop together: by the vote, or at its end, each with its own last wait)
+        if (ok) ok = pf_wait(&ofull[t], 0u, abort_flag, lim);
+        tops[half * 128 + r] = l;
+        if (!vote(!ok)) {
             tc_fence_after_sync();
             write_o();
-            if (store) p.ml[at] = make_float2(m, l);
+            if (store && half == 0) p.ml[at] = make_float2(m, l + tops[128 + r]);
             tc_fence_before_sync();
         }
     }

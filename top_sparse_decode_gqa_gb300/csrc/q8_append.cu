@@ -90,7 +90,6 @@ __global__ void __launch_bounds__(kAppendThreads) q8_append_kernel(const AppendP
     const int kv = hv >= (unsigned)p.Hkv ? 1 : 0;
     const unsigned h = hv - (kv ? (unsigned)p.Hkv : 0u);
     pdl_wait();  // the new rows may come from the preceding kernel
-    pdl_launch_dependents();
     const int first = p.pos0[b], cnt = min(p.n, p.count != nullptr ? p.count[b] : p.n);
     const long long sn = kv ? p.sn[1] : p.sn[0];
     const uint8_t* src = (kv ? p.src[1] : p.src[0]) +

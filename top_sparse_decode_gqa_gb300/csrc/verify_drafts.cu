@@ -177,7 +177,6 @@ __global__ void __launch_bounds__(kVdThreads, 2) verify_kernel(const VerifyParam
     const int C = p.ctas, rank = (int)blockIdx.x % C, b = (int)blockIdx.x / C;
     const int V = p.V, N = p.N;
     pdl_wait();  // the probabilities are the preceding kernels' results
-    pdl_launch_dependents();
     const int n = p.count != nullptr ? max(0, min(V, p.count[b])) : V;
     if (warp == 0) {
         int a = n;
