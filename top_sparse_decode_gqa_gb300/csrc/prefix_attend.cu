@@ -18,12 +18,17 @@
 // tensor cores waited for; S is read twice, 32 columns at a time, which leaves the 16 warps 96
 // registers a thread), P_t back into the TMEM columns S_t held (32 keys: 16 columns of one
 // bf16 part, 16 of the other), O_t += P_t V with P from TMEM and V as it lies in memory
-// (MN-major).  The MMA warp alternates the tiles, so the tensor cores work on one while the other's
-// softmax runs.  O_t is rescaled only when a row's maximum has grown by more than 2^8 since the last time
+// (MN-major).  One MMA warp alternates the tiles, so the tensor cores work on one while the other's
+// softmax runs (a warp a tile lets both tiles fall into step: 153 -> 181 us).  That warp does as little else
+// as it can, since what it does between MMAs the tensor cores wait for: its waits are one wait, a lane
+// a barrier, and a stage is given back by the softmax threads, whose wait for the scores tells the same.  O_t is rescaled only when a row's maximum has grown by more than 2^8 since the last time
 // (weights stay below 2^8; the quotient O / l does not change), which is rare after the first tiles.
 // The tensor cores cut what they add to a sum (2^-24 of it), so SD_F32 output starts O_t anew every
 // 16 tiles and adds up in fp32 in the workspace (L2).  The softmax takes 4 to 5 instructions an
 // element: products and sums two at a time (f32x2), three-way maxima.
+// Several pairs of row tiles read the same key tiles side by side, from L2.  (Clusters of two CTAs that load
+// half of every key tile for both were slower, 137 -> 175 us for 1024 rows a KV head: each then
+// waits for the other's stages.  So was asking L2 for tiles ahead.)
 // TMEM: S_0, S_1 (128 columns each), O_0, O_1 (d each).  Shared memory: 2 Q tiles, 2 stages of K
 // and of V.  Every wait is bounded; a wait that runs out raises an abort flag, the copies and MMAs
 // in flight land, and the kernel frees its TMEM and returns.
@@ -95,15 +100,19 @@ SD_DEVINL float max3(float a, float b, float c) {
     return r;
 }
 
-// A bounded wait that gives up (within its limit) and raises the abort flag for the others.
+// A bounded wait that gives up (within its limit) and raises the abort flag for the others.  The clock
+// is read once in 256 tries only: reading it takes as long as a whole step of the pipeline.
 SD_DEVINL bool pf_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, uint64_t lim) {
-    if (mbar_try_wait(bar, parity)) return true;
-    const uint64_t t0 = globaltimer_ns();
+    uint64_t t0 = 0;
     for (uint32_t i = 1;; ++i) {
         if (mbar_try_wait(bar, parity)) return true;
-        if ((i & 63u) == 0u && (*abort_flag || globaltimer_ns() - t0 > lim)) {
-            *abort_flag = 1;
-            return false;
+        if ((i & 255u) == 0u) {
+            const uint64_t now = globaltimer_ns();
+            if (t0 == 0) t0 = now;
+            if (*abort_flag || now - t0 > lim) {
+                *abort_flag = 1;
+                return false;
+            }
         }
     }
 }
@@ -118,10 +127,11 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     uint8_t* sm = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
     uint64_t* qfull = reinterpret_cast<uint64_t*>(sm + L::oBars);
     uint64_t* kfull = qfull + 1;
-    uint64_t* kempty = kfull + kPfStages;
-    uint64_t* vfull = kempty + kPfStages;
-    uint64_t* vempty = vfull + kPfStages;
-    uint64_t* sfull = vempty + kPfStages;  // [2] S_t is in TMEM (and O_t += P_t V of the tile before is done)
+    uint64_t* vfull = kfull + kPfStages;
+    // [2] event e, on barrier e % 2: every row tile's S(e) and O += P(e - 1) V are done, so the stages of K(e)
+    // and V(e - 1) are free
+    uint64_t* freed = vfull + kPfStages;
+    uint64_t* sfull = freed + 2;  // [2] S_t is in TMEM (and O_t += P_t V of the tile before is done)
     uint64_t* pfull = sfull + 2;           // [2] P_t is in TMEM
     uint64_t* ofull = pfull + 2;           // [2] the last O_t is done
     uint64_t* drain = ofull + 2;
@@ -136,12 +146,12 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     const uint64_t lim = p.wait_ns;
 
     if (tid == 0) {
+        static_assert(kPfStages == 2, "an event's barrier follows the stage's");
         mbar_init(qfull, 1);
         for (int s = 0; s < kPfStages; ++s) {
             mbar_init(&kfull[s], 1);
-            mbar_init(&kempty[s], 1);
             mbar_init(&vfull[s], 1);
-            mbar_init(&vempty[s], 1);
+            mbar_init(&freed[s], (uint32_t)nq);  // a stage is free once both row tiles are done with it
         }
         for (int t = 0; t < 2; ++t) {
             mbar_init(&sfull[t], 1);
@@ -157,6 +167,11 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem = *tmem_slot;
+    auto load_tile = [&](uint8_t* dst, const CUtensorMap* map, int key, uint64_t* bar) {
+        mbar_arrive_expect_tx(bar, L::kTile);
+#pragma unroll
+        for (int a = 0; a < L::kAtoms; ++a) tma_load_3d(dst + a * L::kAtom, map, 64 * a, key, kvh, bar);
+    };
     pdl_wait();  // q and the prefix may be the preceding kernels' results
     pdl_launch_dependents();
 
@@ -170,84 +185,81 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                 for (int a = 0; a < L::kAtoms; ++a)
                     tma_load_3d(sm + L::oQ + t * L::kTile + a * L::kAtom, &qmap, 64 * a, kvh * p.G,
                                 (2 * pair + t) * p.bpt, qfull);
+            auto event = [&](int e) {  // event e has happened (those before the first tile have)
+                return e < 0 || pf_wait(&freed[e & 1], (uint32_t)(e >> 1) & 1u, abort_flag, lim);
+            };
             for (int n = 0; n < nt; ++n) {
                 const int s = n % kPfStages;
-                const uint32_t ph = ((uint32_t)(n / kPfStages) & 1u) ^ 1u;
                 const int key = (n0 + n) * kPfKeys;
-                if (!pf_wait(&kempty[s], ph, abort_flag, lim)) {
-                    *abort_flag = 1;
-                    break;
-                }
-                mbar_arrive_expect_tx(&kfull[s], L::kTile);
-#pragma unroll
-                for (int a = 0; a < L::kAtoms; ++a)
-                    tma_load_3d(sm + L::oK + s * L::kTile + a * L::kAtom, &kmap, 64 * a, key, kvh, &kfull[s]);
+                if (!event(n - 2)) break;
+                load_tile(sm + L::oK + s * L::kTile, &kmap, key, &kfull[s]);
                 issued = 2 * n + 1;
-                if (!pf_wait(&vempty[s], ph, abort_flag, lim)) {
-                    *abort_flag = 1;
-                    break;
-                }
-                mbar_arrive_expect_tx(&vfull[s], L::kTile);
-#pragma unroll
-                for (int a = 0; a < L::kAtoms; ++a)
-                    tma_load_3d(sm + L::oV + s * L::kTile + a * L::kAtom, &vmap, 64 * a, key, kvh, &vfull[s]);
+                if (!event(n - 1)) break;
+                load_tile(sm + L::oV + s * L::kTile, &vmap, key, &vfull[s]);
                 issued = 2 * n + 2;
             }
         }
     } else if (warp == kPfMma) {
-        if (lane == 0) {
-            constexpr uint32_t kIdS = umma_idesc_bf16_f32(kPfRows, kPfKeys);
-            constexpr uint32_t kIdO = umma_idesc_bf16_f32(kPfRows, D) | kUmmaBMnMajor;
-            const uint32_t base = smem_addr(sm);
-            auto scores = [&](int t, int n) {  // S_t = Q_t K_n^T
-                const uint32_t a0 = base + L::oQ + t * L::kTile, b0 = base + L::oK + (n % kPfStages) * L::kTile;
+        // the whole warp runs along, one elected lane issues
+        constexpr uint32_t kIdS = umma_idesc_bf16_f32(kPfRows, kPfKeys);
+        constexpr uint32_t kIdO = umma_idesc_bf16_f32(kPfRows, D) | kUmmaBMnMajor;
+        const uint32_t base = smem_addr(sm);
+        const uint64_t qd = umma_desc_k_sw128(base + L::oQ), kd = umma_desc_k_sw128(base + L::oK);
+        const uint64_t vd = umma_desc_mn_sw128(base + L::oV, L::kAtom);
+        constexpr uint64_t kStep = L::kTile >> 4;  // a tile, in a descriptor's address field
+        auto scores = [&](int t, int n) {  // S_t = Q_t K_n^T
+            const uint64_t a = qd + t * kStep, b = kd + (n % kPfStages) * kStep;
 #pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
-                    const uint32_t off = (uint32_t)((k >> 2) * L::kAtom + (k & 3) * 32);
-                    umma_bf16(tmem + t * 128, umma_desc_k_sw128(a0 + off), umma_desc_k_sw128(b0 + off), kIdS,
-                              k > 0 ? 1u : 0u);
-                }
-                umma_commit(&sfull[t]);
-            };
-            auto output = [&](int t, int n) {  // O_t += P_t V_n
-                const uint32_t b0 = base + L::oV + (n % kPfStages) * L::kTile;
-                const uint32_t o = tmem + 256 + t * 128, a = tmem + t * 128;
-#pragma unroll
-                for (int k = 0; k < kPfKeys / 16; ++k) {
-                    const uint64_t bd = umma_desc_mn_sw128(b0 + k * 2048, L::kAtom);
-                    const uint32_t ak = a + 32 * (k >> 1) + 8 * (k & 1);
-                    umma_bf16_ta(o, ak, bd, kIdO, (HILO ? n % kPfFold : n) > 0 || k > 0 ? 1u : 0u);
-                    if (HILO) umma_bf16_ta(o, ak + 16, bd, kIdO, 1u);
-                }
-            };
-            bool ok = pf_wait(qfull, 0u, abort_flag, lim) && pf_wait(&kfull[0], 0u, abort_flag, lim);
-            if (ok) {
-                tc_fence_after_sync();
-                for (int t = 0; t < nq; ++t) scores(t, 0);
-                umma_commit(&kempty[0]);
+            for (int k = 0; k < D / 16; ++k) {
+                constexpr uint64_t kAt = L::kAtom >> 4;
+                const uint64_t off = (k >> 2) * kAt + (k & 3) * 2;
+                umma_bf16(tmem + t * 128, a + off, b + off, kIdS, k > 0 ? 1u : 0u);
             }
-            for (int n = 0; ok && n < nt; ++n) {
-                const uint32_t ph = (uint32_t)(n / kPfStages) & 1u;
-                const uint32_t phn = (uint32_t)((n + 1) / kPfStages) & 1u;
-                ok = pf_wait(&vfull[n % kPfStages], ph, abort_flag, lim);
-                if (ok && n + 1 < nt) ok = pf_wait(&kfull[(n + 1) % kPfStages], phn, abort_flag, lim);
-                for (int t = 0; ok && t < nq; ++t) {
-                    ok = pf_wait(&pfull[t], (uint32_t)n & 1u, abort_flag, lim);
-                    if (!ok) break;
-                    tc_fence_after_sync();
+            umma_commit(&sfull[t]);
+        };
+        auto output = [&](int t, int n) {  // O_t += P_t V_n
+            const uint64_t b = vd + (n % kPfStages) * kStep;
+            const uint32_t o = tmem + 256 + t * 128, a = tmem + t * 128;
+            const uint32_t add = (HILO ? n % kPfFold : n) > 0 ? 1u : 0u;
+#pragma unroll
+            for (int k = 0; k < kPfKeys / 16; ++k) {
+                const uint32_t ak = a + 32 * (k >> 1) + 8 * (k & 1);
+                umma_bf16_ta(o, ak, b + k * (2048 >> 4), kIdO, k > 0 ? 1u : add);
+                if (HILO) umma_bf16_ta(o, ak + 16, b + k * (2048 >> 4), kIdO, 1u);
+            }
+        };
+        // waits of the warp, lane l for the l-th barrier
+        auto wait_all = [&](uint64_t* b0, uint32_t p0, uint64_t* b1, uint32_t p1, uint64_t* b2, uint32_t p2) {
+            uint64_t* bar = lane == 0 ? b0 : lane == 1 ? b1 : b2;
+            const uint32_t parity = lane == 0 ? p0 : lane == 1 ? p1 : p2;
+            const bool got = __all_sync(0xffffffffu, pf_wait(bar, parity, abort_flag, lim));
+            tc_fence_after_sync();
+            return got;
+        };
+        bool ok = wait_all(qfull, 0u, &kfull[0], 0u, &kfull[0], 0u);
+        if (ok && elect_one()) {
+            scores(0, 0);
+            if (nq > 1) scores(1, 0);
+        }
+        for (int n = 0; ok && n < nt; ++n) {
+            const int last = n + 1 == nt ? n : n + 1;
+            uint64_t *v = &vfull[n % kPfStages], *k = &kfull[last % kPfStages];
+            const uint32_t pv = (uint32_t)(n / kPfStages) & 1u, pk = (uint32_t)(last / kPfStages) & 1u;
+            for (int t = 0; t < nq; ++t) {
+                ok = wait_all(v, pv, k, pk, &pfull[t], (uint32_t)n & 1u);
+                if (!ok) break;
+                if (elect_one()) {
                     output(t, n);
                     if (n + 1 < nt) scores(t, n + 1);
                     else umma_commit(&ofull[t]);
                 }
-                if (!ok) break;
-                umma_commit(&vempty[n % kPfStages]);
-                if (n + 1 < nt) umma_commit(&kempty[(n + 1) % kPfStages]);
+                __syncwarp();
             }
-            if (!ok) {  // let the MMAs in flight finish before their operands and TMEM go
-                *abort_flag = 1;
-                umma_commit(drain);
-                mbar_wait(drain, 0u, lim);
-            }
+        }
+        if (!ok) {  // let the MMAs in flight finish before their operands and TMEM go
+            *abort_flag = 1;
+            if (elect_one()) umma_commit(drain);
+            mbar_wait(drain, 0u, lim);
         }
     } else if (warp < kPfProd && (warp >> 3) < nq) {
         const int t = warp >> 3, half = (warp >> 2) & 1, quarter = warp & 3;
@@ -305,6 +317,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         for (int n = 0; n < nt; ++n) {
             // every thread reaches the votes whatever its wait came to, so none waits in them for ever
             ok = pf_wait(&sfull[t], (uint32_t)n & 1u, abort_flag, lim);
+            if (ok && (warp & 7) == 0 && lane == 0) mbar_arrive(&freed[n & 1]);  // event n for this row tile
             tc_fence_after_sync();
             if (HILO && n > 0 && n % kPfFold == 0) write_o();
             const int valid = p.P - (n0 + n) * kPfKeys - half * kCols;  // keys of this half within the prefix
@@ -388,7 +401,40 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         tops[half * 128 + r] = l;
         if (!vote(!ok)) {
             tc_fence_after_sync();
-            write_o();
+            if (folded) {
+                write_o();
+            } else {
+                // through the query tile's shared memory (its MMAs are done), an eighth of it a warp: a thread has
+                // a row, a store instruction whole lines of several rows
+                constexpr int kCh = D / 16;  // 16-byte chunks of a row that the warp's part holds (32 rows)
+                uint8_t* st = sm + L::oQ + t * L::kTile + (warp & 7) * (L::kTile / 8);
+                const size_t row0 = ((size_t)kvh * p.splits + split) * p.M + (size_t)(2 * pair + t) * p.G * p.bpt;
+                auto spot = [&](int rr, int ch) { return st + (rr * kCh + (ch ^ ((rr * kCh >> 3) & (kCh - 1)))) * 16; };
+#pragma unroll
+                for (int c = 0; c < kOut / 32; ++c) {
+                    uint32_t o[32];
+                    tmem_ld32_nowait(to + 32 * c, o);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int h = 0; h < 8 / kCh; ++h) {
+                        __syncwarp();
+#pragma unroll
+                        for (int i = 0; i < kCh; ++i) {
+                            const int j = 4 * (h * kCh + i);
+                            *reinterpret_cast<uint4*>(spot(lane, i)) = make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+                        }
+                        __syncwarp();
+                        const int ch = lane & (kCh - 1);
+#pragma unroll
+                        for (int i = 0; i < kCh; ++i) {
+                            const int rr = (32 / kCh) * i + lane / kCh, tr = quarter * 32 + rr;
+                            if (tr < p.G * p.bpt && (2 * pair + t) * p.G * p.bpt + tr < p.M)
+                                *reinterpret_cast<uint4*>(p.o + (row0 + tr) * D + half * kOut + 32 * c + 4 * (h * kCh + ch)) =
+                                    *reinterpret_cast<const uint4*>(spot(rr, ch));
+                        }
+                    }
+                }
+            }
             if (store && half == 0) p.ml[at] = make_float2(m, l + tops[128 + r]);
             tc_fence_before_sync();
         }
@@ -468,9 +514,10 @@ sd_status prefix_launch(const sd_cache_attend_args* a, int splits, const CaWorks
     p.scale_log2 = a->scale * 1.44269504088896340736f;
     p.wait_ns = (unsigned long long)kWaitDeadlineNs;
     const bool hilo = a->out_dtype == SD_F32;
-    auto kern = a->d == 128 ? (hilo ? prefix_kernel<128, true> : prefix_kernel<128, false>)
-                            : (hilo ? prefix_kernel<64, true> : prefix_kernel<64, false>);
-    const int bytes = a->d == 128 ? PfLayout<128>::kBytes : PfLayout<64>::kBytes;
+    const bool d128 = a->d == 128;
+    const auto kern = d128 ? (hilo ? prefix_kernel<128, true> : prefix_kernel<128, false>)
+                           : (hilo ? prefix_kernel<64, true> : prefix_kernel<64, false>);
+    const int bytes = d128 ? PfLayout<128>::kBytes : PfLayout<64>::kBytes;
     SD_CUDA_CHECK(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes),
                   "sd_cache_attend: cudaFuncSetAttribute");
     SD_CUDA_CHECK(launch_pdl(kern, dim3((unsigned)(a->Hkv * s.pairs * splits)), dim3(kPfThreads), (size_t)bytes, st, qmap,

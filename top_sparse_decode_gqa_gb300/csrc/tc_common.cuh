@@ -115,6 +115,17 @@ SD_DEVINL void tma_load_3d(void* dst_smem, const CUtensorMap* map, int x, int y,
         : "memory");
 }
 
+// True for one lane of the warp, which the compiler knows to be one: all lanes call it together.
+SD_DEVINL bool elect_one() {
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(p));
+    return p != 0u;
+}
+
 // Shared-memory matrix descriptor of an MN-major operand in the 128-byte swizzle layout: rows
 // of the K dimension, each 64 neighbouring elements (128 bytes) of the M or N dimension; 8-row groups
 // 1024 bytes apart (stride byte offset), the next 64 elements `chunk_bytes` further (leading
