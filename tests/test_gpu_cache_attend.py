@@ -87,6 +87,41 @@ def test_own_rows(kind, shape, out_dtype):
     run_and_check(*make(kind, *shape), out_dtype)
 
 
+MANY = [  # 17 to 32 query rows a KV head: B, V, Hq, Hkv, d, T, lens
+    (1, 8, 4, 1, 128, 8, [8]),
+    (1, 17, 1, 1, 128, 129, [129]),
+    (1, 32, 2, 2, 128, 128, [127]),
+    (4, 8, 32, 8, 128, 1500, [1500, 8, 700, 4]),      # drafts before the first row
+    (3, 5, 16, 4, 128, 6000, [6000, 0, 257]),         # 20 rows; an empty sequence
+    (40, 8, 8, 2, 128, 300, [(i * 37) % 301 for i in range(40)]),   # more sequences than lanes
+    (1, 8, 4, 1, 128, 40000, [39999]),                # one group over every SM
+    (2, 6, 3, 1, 128, 5000, [4000, 5000]),            # 18 rows
+]
+
+
+@pytest.mark.parametrize("out_dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("shape", MANY, ids=lambda s: "-".join(map(str, s[:6])))
+def test_many_query_rows(kind, shape, out_dtype):
+    run_and_check(*make(kind, *shape, seed=shape[1]), out_dtype)
+
+
+@pytest.mark.parametrize("kind", ["int8", "e4m3"])
+def test_many_query_rows_with_growing_logits_and_scales(kind):
+    """Every tile's largest logit, and its V scales, far above those before: the maxima move at every tile."""
+    B, V, Hq, Hkv, d, T = 1, 8, 4, 1, 128, 3000
+    q, k, v, qpos, kw = make(kind, B, V, Hq, Hkv, d, T, [T], seed=31)
+    x = [torch.randn(1, 1, T, d, device="cuda") for _ in range(2)]
+    ramp = torch.linspace(0, 1, T, device="cuda")[None, None, :, None]
+    x[0] = x[0] * 0.05 + 3.0 * ramp
+    x[1] = x[1] * torch.exp2(40 * ramp - 20)
+    q.copy_((0.3 * q.float() + 0.7).bfloat16())
+    q[0, 3] *= -1.0     # for these the logits fall
+    sd().sd_q8_append(x[0].contiguous(), x[1].contiguous(), k, v, kw["k_scale"], kw["v_scale"],
+                      torch.zeros(1, dtype=torch.int32, device="cuda"))
+    run_and_check(q, k, v, qpos, kw, torch.float32)
+
+
 @pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("V,Hq,Hkv,d,T,block,n_idx", [(1, 8, 2, 128, 640, 1, 100), (1, 4, 4, 64, 640, 16, 7),
                                                       (3, 12, 3, 128, 640, 5, 50), (8, 8, 2, 128, 640, 64, 10)])
