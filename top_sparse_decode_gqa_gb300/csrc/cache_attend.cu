@@ -36,7 +36,9 @@
 // one's are used, V rows likewise, so each load has half a step and the other warps to hide behind.
 //
 // Work: units of 64 rows of one (sequence, KV head), in order, cut into equal runs, one a CTA
-// (all resident at once), whatever the sequences' lengths.  A CTA's run covers one or more
+// (all resident at once), whatever the sequences' lengths.  A group counts for two units more than it has,
+// which is about what its queries, its start and its end cost (without: the CTAs of the shortest of 64
+// sequences of 51 to 512 rows had 8 groups each and set the kernel's time).  A CTA's run covers one or more
 // groups; a group that lies within one run is written directly, the others' states are merged
 // by a second kernel.
 #include <cuda_bf16.h>
@@ -494,6 +496,7 @@ struct CaShared {
     int b;
 };
 
+constexpr unsigned kCaGroupCost = 2;  // (1: 55.4 us, 3: 55.2, 4: 55.5 where 2 takes 54.6)
 constexpr int kFoldSteps = 32;  // steps after which SD_F32 output folds the accumulators
 
 template <int KIND, int D, int NQ, int TS, bool HILO, bool SEL, int MINB>
@@ -517,8 +520,8 @@ __global__ void __launch_bounds__(kCaThreads, MINB) cache_attend_kernel(const Ca
     // (No early trigger for the merge kernel, nor in that one for the next call's: CTAs that wait on an SM
     // keep others from it.  8 ragged e4m3 caches called back to back: 71 us with both, 61 without.)
 
-    // this CTA's run of units: [w0, w1) of all groups' units in order; no run is empty, so a
-    // group's runs are in consecutive slots
+    // this CTA's run of units: [w0, w1) of all groups' units in order.  A group's units are `extra` empty ones,
+    // then its own; the runs that hold own units of a group are consecutive, and so are their slots.
     unsigned W, tb, j, w0;
     int b, kvh;
     const bool few = p.B <= 32;  // lane i knows sequence i: no warp needs another
@@ -537,20 +540,24 @@ __global__ void __launch_bounds__(kCaThreads, MINB) cache_attend_kernel(const Ca
         __syncthreads();
         W = (sh.part[0] + sh.part[1] + sh.part[2] + sh.part[3]) * p.Hkv;
     }
+    const unsigned extra = W > 2u * gridDim.x ? kCaGroupCost : 0u;  // (a unit or two a CTA: nothing to even out)
+    W += (unsigned)p.B * p.Hkv * extra;
     const unsigned ncta = min(gridDim.x, W);
     if (c >= ncta) {
-        if (p.P > 0) pdl_wait();  // (the merge kernel, where there is one, counts on the prefix being done)
+        if (p.P > 0) pdl_wait();  // (the merge kernel counts on the prefix being done)
         return;
     }
     const Cut cut(W, ncta);
     w0 = cut.start(c);
     const unsigned w1 = cut.start(c + 1);
     if constexpr (SEL) {
+        tb += extra;
         const unsigned g = w0 / tb;
         j = w0 - g * tb;
         b = (int)(g / (unsigned)p.Hkv);
         kvh = (int)(g - (unsigned)b * p.Hkv);
     } else if (few) {
+        if (lane < p.B) tl += extra;
         unsigned incl = tl;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -563,11 +570,11 @@ __global__ void __launch_bounds__(kCaThreads, MINB) cache_attend_kernel(const Ca
         kvh = (int)(off / tb);
         j = off - (unsigned)kvh * tb;
     } else {
-        // the sequence of unit w0: sequence i's units start at Hkv * (tiles before it)
+        // the sequence of unit w0: sequence i's units start at Hkv * (units of a group before it)
         unsigned run = 0;
         for (int base = 0; base < p.B; base += kCaThreads) {
             const int i = base + tid;
-            const unsigned t = i < p.B ? tiles_of(seq_len(p, i)) : 0u;
+            const unsigned t = i < p.B ? tiles_of(seq_len(p, i)) + extra : 0u;
             unsigned incl = t;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -590,18 +597,23 @@ __global__ void __launch_bounds__(kCaThreads, MINB) cache_attend_kernel(const Ca
             if (sh.b >= 0) break;
         }
         b = sh.b;
-        tb = tiles_of(seq_len(p, b));
+        tb = tiles_of(seq_len(p, b)) + extra;
         const unsigned off = w0 - sh.base;
         kvh = (int)(off / tb);
         j = off - (unsigned)kvh * tb;
     }
 
     for (unsigned w = w0; w < w1;) {
+        if (j < extra) {
+            w += extra - j;
+            j = extra;
+            if (w >= w1) break;
+        }
         const int g = b * p.Hkv + kvh;
         const int len = seq_len(p, b);
         const unsigned seg = min(tb - j, w1 - w);
         const int list = SEL ? p.n_list : len;
-        const int j0 = (int)j * kCaTile, j1 = len == 0 ? j0 : min(list, j0 + (int)seg * kCaTile);
+        const int j0 = (int)(j - extra) * kCaTile, j1 = len == 0 ? j0 : min(list, j0 + (int)seg * kCaTile);
 
         const uint8_t* kbase = p.kc + (size_t)g * p.T * kRow;
         const uint8_t* vbase = p.vc + (size_t)g * p.T * kRow;
@@ -656,13 +668,15 @@ __global__ void __launch_bounds__(kCaThreads, MINB) cache_attend_kernel(const Ca
                 asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "n"(32 * TS) : "memory");
         };
         // the first steps' rows are on their way while the queries are prepared
-        int rows = resolve(team);
+        int early[kStages];
+#pragma unroll
+        for (int i = 0; i < kStages; ++i) early[i] = resolve(team + i * kTeams);
 #pragma unroll
         for (int i = 0; i + 1 < kStages; ++i) {
-            if (team + i * kTeams < nsteps) fetch(i, rows);
+            if (team + i * kTeams < nsteps) fetch(i, early[i]);
             cp_async_commit();
-            rows = resolve(team + (i + 1) * kTeams);
         }
+        int rows = early[kStages - 1];
 
         // the query rows 8nq + g8 as B fragments, their limits and the smallest limit
         Queries<D, NQ> q;
@@ -813,7 +827,7 @@ __global__ void __launch_bounds__(kCaThreads, MINB) cache_attend_kernel(const Ca
         }
         cp_async_wait<0>();
         __syncthreads();
-        const bool whole = j == 0u && seg == tb && p.P == 0;
+        const bool whole = j == extra && seg == tb - extra && p.P == 0;
         const size_t slot = (size_t)c + g;
         for (int i = tid; i < p.R * (D / 2); i += kCaThreads) {
             const int r = i / (D / 2), d = 2 * (i - r * (D / 2));
@@ -844,14 +858,14 @@ __global__ void __launch_bounds__(kCaThreads, MINB) cache_attend_kernel(const Ca
                 if (d == 0) p.ws.ml[slot * p.R + r] = make_float2(M, L);
             }
         }
-        if (j == 0u && tid == 0)  // the runs that hold the group's units
-            p.ws.meta[g] = make_int2((int)c + g, (int)(cut.run_of(w + tb - 1) - c) + 1);
+        if (j == extra && tid == 0)  // the runs that hold the group's units
+            p.ws.meta[g] = make_int2((int)c + g, (int)(cut.run_of(w + tb - extra - 1) - c) + 1);
         w += seg;
         j = 0;
         if (++kvh == p.Hkv) {
             kvh = 0;
             ++b;
-            if (!SEL && w < w1) tb = tiles_of(seq_len(p, b));
+            if (!SEL && w < w1) tb = tiles_of(seq_len(p, b)) + extra;
         }
     }
     if (p.P > 0) pdl_wait();
@@ -961,7 +975,7 @@ sd_status ca_validate(const sd_cache_attend_args* a, bool pointers) {
     SD_REQUIRE((long)a->B * a->V * a->Hq < (1L << 30) && (long)a->Hkv * a->P < (1L << 31), "%s: too many query or prefix rows",
                who);
     const long rows = a->idx != nullptr ? (long)a->n_idx * a->block : a->T;
-    SD_REQUIRE((long)a->B * a->Hkv * (rows / kCaTile + 1) < (1L << 31), "%s: too many rows", who);
+    SD_REQUIRE((long)a->B * a->Hkv * (rows / kCaTile + 1 + kCaGroupCost) < (1L << 31), "%s: too many rows", who);
     if (!pointers || a->B == 0) return SD_OK;
     SD_REQUIRE(a->q && a->k_cache && a->v_cache && a->qpos && a->out && a->lse, "%s: null pointer", who);
     SD_REQUIRE(a->cache_dtype == SD_BF16 || (a->k_scale && a->v_scale), "%s: an 8-bit cache needs k_scale and v_scale",
