@@ -582,7 +582,7 @@ sd_status sd_q8_append(const sd_q8_append_args* args, void* stream);
  * SD_BF16 (weights rounded once to 8 bits, 11 over an 8-bit cache); lse [B,V,Hq] fp32.  Sums
  * and softmax statistics are fp32.  The split of the work, and so the summation order, depends
  * on the sizes, qpos and the GPU, not on the data; equal calls give equal bits.
- * Limits: d in {64, 128}, G*V <= 32 (G = Hq/Hkv), B <= 65535.
+ * Limits: d in {64, 128}, G*V <= 32 (G = Hq/Hkv), B <= 65535, T, P and n_idx*block <= 2^30.
  * The workspace (sd_cache_attend_workspace_bytes, a host computation over the sizes; 256-byte
  * aligned) holds the partial states that the call's last kernel merges; no initialisation; calls
  * sharing one must not overlap on the GPU.  Launched as programmatic dependents of the preceding

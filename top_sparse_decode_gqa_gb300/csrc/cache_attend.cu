@@ -125,7 +125,7 @@ SD_DEVINL void mma16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint3
         mma_bf16_16816(d, a0, a1, a2, a3, b0, b1);
 }
 
-SD_DEVINL uint4 ld_row16(const uint8_t* p) { return __ldg(reinterpret_cast<const uint4*>(p)); }
+SD_DEVINL uint4 ld_row16(const uint8_t* p) { return *reinterpret_cast<const uint4*>(p); }
 
 // A step's 16 rows of K and V in shared memory: 16-byte chunk c of row r of either lies at r * kRow
 // + ((c ^ swizzle(r)) << 4), K first, then the rows' scales (K, V) and positions.
@@ -685,7 +685,7 @@ __global__ void __launch_bounds__(kCaThreads, MINB) cache_attend_kernel(const Ca
         __syncthreads();  // (the segment before is done with the limits and the states)
         int lmin = p.T;  // rows every query sees
         if (tid < 8 * NQ * TS) sh.lim[tid] = tid < p.R ? min(p.qpos[(size_t)b * p.V + tid / p.G], p.T - 1) : -1;
-        for (int v = 0; v < p.V; ++v) lmin = min(lmin, p.qpos[(size_t)b * p.V + v] + 1);
+        for (int v = 0; v < p.V; ++v) lmin = min(lmin, min(p.qpos[(size_t)b * p.V + v], p.T - 1) + 1);
 #pragma unroll
         for (int nt = 0; nt < (Queries<D, NQ>::kShared ? TS * NQ : NQ); ++nt) {
             if (Queries<D, NQ>::kShared && warp != nt) continue;  // tile nt is warp nt's to prepare
@@ -958,10 +958,11 @@ sd_status ca_validate(const sd_cache_attend_args* a, bool pointers) {
     SD_REQUIRE(a->cache_dtype == SD_BF16 || a->cache_dtype == SD_I8 || a->cache_dtype == SD_E4M3,
                "%s: cache_dtype must be SD_BF16, SD_I8 or SD_E4M3", who);
     SD_REQUIRE(a->out_dtype == SD_F32 || a->out_dtype == SD_BF16, "%s: out_dtype must be SD_F32 or SD_BF16", who);
-    SD_REQUIRE(a->B >= 0 && a->V >= 1 && a->Hkv >= 1 && a->Hq >= 1 && a->Hq % a->Hkv == 0 && a->T >= 1 && a->P >= 0,
+    SD_REQUIRE(a->B >= 0 && a->V >= 1 && a->Hkv >= 1 && a->Hq >= 1 && a->Hq % a->Hkv == 0 && a->T >= 1 && a->P >= 0 &&
+                   a->T <= (1 << 30) && a->P <= (1 << 30),
                "%s: bad sizes (B=%d V=%d Hq=%d Hkv=%d T=%d P=%d)", who, a->B, a->V, a->Hq, a->Hkv, a->T, a->P);
     SD_REQUIRE(a->B <= 65535 && a->Hq <= 65535, "%s: B and Hq must be <= 65535", who);
-    SD_REQUIRE(a->idx == nullptr || (a->n_idx >= 0 && a->block >= 1 && (long)a->n_idx * a->block < (1L << 31)),
+    SD_REQUIRE(a->idx == nullptr || (a->n_idx >= 0 && a->block >= 1 && (long)a->n_idx * a->block <= (1L << 30)),
                "%s: bad selection (n_idx=%d block=%d)", who, a->n_idx, a->block);
     if (a->d != 64 && a->d != 128) {
         set_error("%s: d must be 64 or 128 (got %d)", who, a->d);

@@ -42,8 +42,8 @@ template <int SRC>  // 8 elements of a row in fp32 (sd_dtype)
 struct Eight {
     uint4 r[SRC == SD_F32 ? 2 : 1];
     SD_DEVINL void load(const uint8_t* p) {
-        r[0] = __ldg(reinterpret_cast<const uint4*>(p));
-        if constexpr (SRC == SD_F32) r[1] = __ldg(reinterpret_cast<const uint4*>(p) + 1);
+        r[0] = *reinterpret_cast<const uint4*>(p);
+        if constexpr (SRC == SD_F32) r[1] = reinterpret_cast<const uint4*>(p)[1];
     }
     SD_DEVINL void zero() {
         r[0] = make_uint4(0u, 0u, 0u, 0u);

@@ -179,25 +179,30 @@ __global__ void __launch_bounds__(kVdThreads, 2) verify_kernel(const VerifyParam
     pdl_wait();  // the probabilities are the preceding kernels' results
     const int n = p.count != nullptr ? max(0, min(V, p.count[b])) : V;
     if (warp == 0) {
+        // (the drafts' loads wait for nothing, n least of all: what is past it is left out)
         int a = n;
-        for (int base = 0; base < n && a == n; base += 32) {
+        for (int base = 0; base < V; base += 32) {
             const int i = base + lane;
-            bool no = false;
-            if (i < n) {
-                const int x = p.draft[(size_t)b * V + i];
-                const float u = p.u[(size_t)b * V + i];
-                no = true;
-                if (x >= 0 && x < N) {
-                    // products of two fp32 numbers are exact in fp64
-                    const double px = prob_at<DT>(p.p, ((size_t)b * (V + 1) + i) * N + x);
-                    const double qx = p.q != nullptr ? prob_at<DT>(p.q, ((size_t)b * V + i) * N + x) : 1.f;
-                    no = !((double)u * qx < px);
-                } else if (rank == 0) {
-                    report(p.err, SD_DEVERR_INDEX);
-                }
+            int x = -1;
+            float u = 0.f, px = 0.f, qx = 1.f;
+            if (i < V) {
+                x = p.draft[(size_t)b * V + i];
+                u = p.u[(size_t)b * V + i];
             }
+            const bool in = x >= 0 && x < N;
+            if (in) {
+                px = prob_at<DT>(p.p, ((size_t)b * (V + 1) + i) * N + x);
+                if (p.q != nullptr) qx = prob_at<DT>(p.q, ((size_t)b * V + i) * N + x);
+            }
+            if (i < n && !in && rank == 0) report(p.err, SD_DEVERR_INDEX);
+            // products of two fp32 numbers are exact in fp64
+            const bool no = i < n && !(in && (double)u * (double)qx < (double)px);
             const unsigned m = __ballot_sync(0xffffffffu, no);
-            if (m != 0u) a = base + __ffs(m) - 1;
+            if (m != 0u) {
+                a = base + __ffs(m) - 1;
+                break;
+            }
+            if (base + 32 >= n) break;
         }
         if (lane == 0) s_accept = a;
     }
@@ -223,7 +228,8 @@ __global__ void __launch_bounds__(kVdThreads, 2) verify_kernel(const VerifyParam
         if (lane == 0) wsum[warp] = sum;
         cluster.sync();
         if (tid < parts) all[tid] = *cluster.map_shared_rank(&wsum[tid % kVdWarps], tid / kVdWarps);
-        cluster.sync();  // (also: nobody leaves or writes wsum again while another CTA reads it)
+        cluster.barrier_arrive();  // (waited for where this CTA would write wsum again or leave)
+        __syncthreads();
         if (warp == 0) {
             constexpr int kPer = kVdMaxCtas * kVdWarps / 32;
             unsigned long long v[kPer], mine = 0ull;
@@ -253,6 +259,7 @@ __global__ void __launch_bounds__(kVdThreads, 2) verify_kernel(const VerifyParam
         }
         __syncthreads();
         if (s_total != 0ull || mode == 1) break;
+        cluster.barrier_wait();
         w.q = nullptr;  // p and q are equal (no residual): the target itself
         w.skip = -1;
         __syncthreads();
@@ -266,7 +273,10 @@ __global__ void __launch_bounds__(kVdThreads, 2) verify_kernel(const VerifyParam
             if (s_total == 0ull) out[a] = -1;  // a row of zeros: no token
         }
     }
-    if (s_total == 0ull || s_cross / kVdWarps != rank) return;
+    if (s_total == 0ull || s_cross / kVdWarps != rank) {
+        cluster.barrier_wait();
+        return;
+    }
     // the part of warp s_cross: a scan over it, 4 entries a thread
     const int lo = s_cross * part, hi = min(N, lo + part);
     const unsigned long long thr = s_thr;
@@ -294,8 +304,9 @@ __global__ void __launch_bounds__(kVdThreads, 2) verify_kernel(const VerifyParam
         }
         below += whole;
         __syncthreads();
-        if (s_found) return;
+        if (s_found) break;
     }
+    cluster.barrier_wait();
 }
 
 template <int DT>
