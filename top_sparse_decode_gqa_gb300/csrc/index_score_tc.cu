@@ -246,21 +246,6 @@ bool make_tensor_map_2d(CUtensorMap* m, const void* base, uint64_t nrows, int d,
     return r == CUDA_SUCCESS;
 }
 
-// 3-D tensor map of bf16 elements over [n2, n1, d] (row-major), box = 64 columns x box1 x box2,
-// 128-byte swizzle, zero fill outside every dimension.
-bool make_tensor_map_3d(CUtensorMap* m, const void* base, uint64_t n2, uint64_t n1, int d, int box2, int box1) {
-    auto fn = encode_fn();
-    if (fn == nullptr) return false;
-    cuuint64_t dims[3] = {(cuuint64_t)d, n1, n2};
-    cuuint64_t strides[2] = {(cuuint64_t)d * 2, n1 * (cuuint64_t)d * 2};
-    cuuint32_t box[3] = {64, (cuuint32_t)box1, (cuuint32_t)box2};
-    cuuint32_t estr[3] = {1, 1, 1};
-    CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
-                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS;
-}
-
 // bf16 (or fp16) keys and queries of the same type on the tensor cores; d_idx in {64, 128},
 // V <= 16.  per_query: every query row gets its own score row (rows*V of them) instead of
 // the max over V.

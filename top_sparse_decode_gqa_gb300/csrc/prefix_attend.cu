@@ -32,11 +32,13 @@
 // TMEM: S_0, S_1 (128 columns each), O_0, O_1 (d each).  Shared memory: 2 Q tiles, 2 stages of K
 // and of V.  Every wait is bounded; a wait that runs out raises an abort flag, the copies and MMAs
 // in flight land, and the kernel frees its TMEM and returns.
+#include <cudaTypedefs.h>
+
+#include <atomic>
 #include <cmath>
 
 #include "cache_attend.cuh"
-#include "step_tiles.cuh"
-#include "tc_common.cuh"
+#include "tc_operands.cuh"
 
 namespace sd {
 namespace {
@@ -72,33 +74,6 @@ struct PfParams {
     float scale_log2;
     unsigned long long wait_ns;
 };
-
-// Two fp32 operations in one instruction.
-SD_DEVINL uint64_t pack2(float x, float y) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
-    return r;
-}
-SD_DEVINL float2 unpack2(uint64_t v) {
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-    return r;
-}
-SD_DEVINL uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-SD_DEVINL uint64_t add2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-SD_DEVINL float max3(float a, float b, float c) {
-    float r;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-    return r;
-}
 
 // A bounded wait that gives up (within its limit) and raises the abort flag for the others.  The clock
 // is read once in 256 tries only: reading it takes as long as a whole step of the pipeline.
@@ -455,6 +430,30 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         tc_fence_after_sync();
         tmem_dealloc(tmem, 512);
     }
+}
+
+// 3-D tensor map of bf16 elements over [n2, n1, d] (row-major), box = 64 columns x box1 x box2,
+// 128-byte swizzle, zero fill outside every dimension.
+bool make_tensor_map_3d(CUtensorMap* m, const void* base, uint64_t n2, uint64_t n1, int d, int box2, int box1) {
+    static std::atomic<PFN_cuTensorMapEncodeTiled_v12000> found{nullptr};
+    auto fn = found.load(std::memory_order_relaxed);
+    if (fn == nullptr) {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult q{};
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            return false;
+        fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+        found.store(fn, std::memory_order_relaxed);
+    }
+    cuuint64_t dims[3] = {(cuuint64_t)d, n1, n2};
+    cuuint64_t strides[2] = {(cuuint64_t)d * 2, n1 * (cuuint64_t)d * 2};
+    cuuint32_t box[3] = {64, (cuuint32_t)box1, (cuuint32_t)box2};
+    cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
 }
 
 struct PfShape {

@@ -80,10 +80,6 @@ inline sd_status launch_status(const char* what) {
 // when the driver's encoder is unavailable or rejects the map.
 bool make_tensor_map_2d(CUtensorMap* m, const void* base, uint64_t nrows, int d, int box_rows, bool f16);
 
-// 3-D tensor map of bf16 elements over [n2, n1, d] (row-major), box = 64 columns x box1 x box2,
-// 128-byte swizzle, zero fill outside every dimension.
-bool make_tensor_map_3d(CUtensorMap* m, const void* base, uint64_t n2, uint64_t n1, int d, int box2, int box1);
-
 // The indexer on the tensor cores (index_score_tc.cu): bf16 keys and queries, or fp16 ones
 // (f16).
 sd_status index_score_tc_launch(const void* q_idx, const void* k_idx, int rows, int V, int N, int d_idx,
