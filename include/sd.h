@@ -576,8 +576,9 @@ sd_status sd_q8_append(const sd_q8_append_args* args, void* stream);
  * the cache are skipped and set SD_DEVERR_INDEX; an entry given twice counts twice.
  * q [B,V,Hq,d] bf16; k_cache, v_cache [B,Hkv,T,d] of cache_dtype (SD_BF16, SD_I8 or SD_E4M3);
  * k_scale, v_scale [B,Hkv,T] fp32, finite and >= 0 (8-bit caches only); k_prefix, v_prefix
- * [Hkv,P,d] bf16 (P = 0: none).  Attended bf16 rows are finite; so are rows up to the largest
- * qpos of their sequence.  Rows beyond it, and their scales, may hold anything.
+ * [Hkv,P,d] bf16 (P = 0: none).  q, attended rows and their scales are finite, logits within
+ * +-1e30.  Rows that no query token attends (beyond its sequence's largest qpos, or not in
+ * idx), and their scales, may hold anything.
  * out [B,V,Hq,d] of out_dtype: SD_F32 (softmax weights kept to 16 or more significant bits) or
  * SD_BF16 (weights rounded once to 8 bits, 11 over an 8-bit cache); lse [B,V,Hq] fp32.  Sums
  * and softmax statistics are fp32.  The split of the work, and so the summation order, depends

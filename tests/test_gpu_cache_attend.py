@@ -135,6 +135,32 @@ def test_selected_rows(kind, V, Hq, Hkv, d, T, block, n_idx):
     run_and_check(*x, torch.float32, idx=idx.contiguous(), block=block)
 
 
+@pytest.mark.parametrize("out_dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("V,Hq,Hkv,d,block", [(1, 8, 2, 128, 1), (1, 4, 2, 64, 5), (8, 4, 2, 128, 5), (4, 8, 2, 64, 1)])
+def test_rows_that_are_not_selected_may_hold_anything(kind, V, Hq, Hkv, d, block, out_dtype):
+    """NaN, infinities and the largest codes in every row that idx leaves out, row 0 first of all: an empty
+    slot, a list that ends inside a step and one without any row read nothing of them."""
+    B, T, n_idx = 3, 200, 7
+    q, k, v, qpos, kw = make(kind, B, V, Hq, Hkv, d, T, [200, 150, 200], seed=40 + V)
+    g = torch.Generator("cuda").manual_seed(41)
+    idx = (torch.rand(B, Hkv, T // block - 1, device="cuda", generator=g).topk(n_idx, -1).indices + 1).to(torch.int32)
+    idx[0, 0, 2] = -1
+    idx[2, 1] = -1          # nothing selected at all
+    out_of = torch.ones(B, Hkv, T, dtype=torch.bool, device="cuda")
+    for b in range(B):
+        for h in range(Hkv):
+            e = idx[b, h][idx[b, h] >= 0].long()
+            out_of[b, h, (e[:, None] * block + torch.arange(block, device="cuda")).reshape(-1)] = False
+    assert bool(out_of[:, :, 0].all())
+    if kind == "bf16":
+        k[out_of], v[out_of] = math.nan, math.inf
+    else:
+        k.view(torch.uint8)[out_of], v.view(torch.uint8)[out_of] = 0x7f, 0x7f   # e4m3: NaN
+        kw["k_scale"][out_of], kw["v_scale"][out_of] = math.nan, math.inf
+    run_and_check(q, k, v, qpos, kw, out_dtype, idx=idx, block=block)
+
+
 def test_bad_indices_are_skipped_and_reported():
     q, k, v, qpos, kw = make("int8", 1, 1, 4, 1, 128, 64, [64])
     idx = torch.tensor([[[3, 64, 9, -2, 2147483647, 5]]], dtype=torch.int32, device="cuda")
@@ -198,6 +224,16 @@ def test_equal_calls_give_equal_bits_and_leave_nothing_behind():
     sd().sd_cache_attend(a)
     torch.cuda.synchronize()
     assert torch.equal(o1, first[0]) and torch.equal(l1, first[1])
+
+
+def test_a_stream_given_by_its_handle():
+    x = make("int8", 3, 2, 8, 2, 128, 500, [500, 3, 400], seed=9)
+    want = sd().cache_attend(*x[:4], **x[4])
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    got = sd().cache_attend(*x[:4], stream=s.cuda_stream, **x[4])
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
 def test_capture_and_replay_with_growing_sequences():

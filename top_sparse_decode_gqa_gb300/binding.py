@@ -780,7 +780,9 @@ def cache_attend(q, k_cache, v_cache, qpos, workspace=None, stream=None, **kw):
     a, out, lse = make_cache_attend_args(q, k_cache, v_cache, qpos, **kw)
     if workspace is None:
         # made (for the allocator) on the stream of the call
-        with torch.cuda.stream(stream) if isinstance(stream, torch.cuda.Stream) else contextlib.nullcontext():
+        if stream is not None and not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(_stream(stream).value or 0)
+        with torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext():
             workspace = cache_attend_workspace(a)
     a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     sd_cache_attend(a, stream)

@@ -25,15 +25,15 @@
 //
 // Bound: HBM; for more than 16 query rows the tensor cores' mma.sync rate comes close (8 cycles an
 // instruction: 174 us against 163 us of loads for 4 x 131072 int8 rows and 32 query rows in two-part
-// weights).  So that little but the loads takes time, the rows go from global memory straight
-// into registers in the operand layout of mma.sync m16n8k16, with no shared memory: the
-// contraction over d may run in any order, so a lane takes 16 neighbouring bytes of its K rows as
-// its elements of four k-steps (the query fragments are permuted alike), and the output columns
-// may be in any order, so it takes 16 neighbouring columns of its four V rows.  Every load
-// instruction then covers whole 64- or 128-byte lines.  S^T = K Q^T and O^T = V^T P^T put the 16
-// rows of a step on the M side and 8 query rows on the N side (NQ = 1, 2 or 4 of them in one warp:
-// a row's codes are widened once for all).  The next step's K rows are fetched as soon as this
-// one's are used, V rows likewise, so each load has half a step and the other warps to hide behind.
+// weights).  A warp takes 8 or 16 query rows; for 17 to 32 two warps make a team that shares the
+// fetched rows.  A team copies its steps of 16 K and V rows into a ring of 2 or 3 stages of its own
+// (cp.async), so loads of the next steps are in flight through this one's arithmetic and no barrier is
+// wider than a team.  The contraction over d may run in any order, so a lane takes 16 neighbouring
+// bytes of its K rows as its elements of four k-steps of mma.sync m16n8k16 (the query fragments are
+// permuted alike), and the output columns may be in any order, so it takes neighbouring columns of
+// its four V rows: whole 8- or 16-byte reads, spread over the banks by a swizzle and the order of rows.
+// S^T = K Q^T and O^T = V^T P^T put the 16 rows of a step on the M side and 8 query rows on the N
+// side: a row's codes are widened once for all the query rows of the warp.
 //
 // Work: units of 64 rows of one (sequence, KV head), in order, cut into equal runs, one a CTA
 // (all resident at once), whatever the sequences' lengths.  A group counts for two units more than it has,
@@ -123,6 +123,12 @@ SD_DEVINL void mma16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint3
         mma_f16_16816(d, a0, a1, a2, a3, b0, b1);
     else
         mma_bf16_16816(d, a0, a1, a2, a3, b0, b1);
+}
+
+// 4-byte cp.async that copies src_size (0 or 4) bytes and fills the rest with zeros.
+SD_DEVINL void cp_async4_zfill(void* dst_smem, const void* src, uint32_t src_size) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_addr(dst_smem)), "l"(src), "r"(src_size)
+                 : "memory");
 }
 
 SD_DEVINL uint4 ld_row16(const uint8_t* p) { return *reinterpret_cast<const uint4*>(p); }
@@ -643,21 +649,24 @@ __global__ void __launch_bounds__(kCaThreads, MINB) cache_attend_kernel(const Ca
             return t;
         };
         // Copies the team's rows of a step (resolved in `rows`) into a stage of its ring, a row that is none
-        // as row 0, which some query sees.  A team of two shares the copies: K, V.
+        // as zeros (whatever the cache holds there, its weight of 0 must not meet a NaN or an infinity).
+        // A team of two shares the copies: K, V.
         auto fetch = [&](int stage, int rows) {
             uint8_t* st = sh.ring[team][stage];
             constexpr int kPer = 32 / S::kChunks > 0 ? 32 / S::kChunks : 1;  // rows an instruction copies
             const int c0 = lane % S::kChunks, r0 = lane / S::kChunks;
 #pragma unroll
             for (int r = 0; r < 16; r += kPer) {
-                const int t = max(__shfl_sync(0xffffffffu, rows, r + r0), 0);
-                const size_t off = (size_t)t * kRow + 16 * c0;
+                const int t = __shfl_sync(0xffffffffu, rows, r + r0);
+                const size_t off = (size_t)max(t, 0) * kRow + 16 * c0;
+                const uint32_t n = t < 0 ? 0u : 16u;
                 const int to = S::at(r + r0, c0);
-                if (TS == 1 || half == 0) cp_async16(st + to, kbase + off);
-                if (TS == 1 || half == 1) cp_async16(st + S::oV + to, vbase + off);
+                if (TS == 1 || half == 0) cp_async16_zfill(st + to, kbase + off, n);
+                if (TS == 1 || half == 1) cp_async16_zfill(st + S::oV + to, vbase + off, n);
             }
             if (half == 0) {
-                if constexpr (F16) cp_async4(st + S::oKs + 4 * lane, (lane < 16 ? ksb : vsb) + max(rows, 0));
+                if constexpr (F16)
+                    cp_async4_zfill(st + S::oKs + 4 * lane, (lane < 16 ? ksb : vsb) + max(rows, 0), rows < 0 ? 0u : 4u);
                 if (lane < 16) reinterpret_cast<int*>(st + S::oPos)[lane] = rows < 0 ? 0x7fffffff : rows;
             }
         };
