@@ -324,6 +324,31 @@ def test_shared_prefix(kind, shape, out_dtype):
     run_and_check_prefix(x, kp, vp, out_dtype)
 
 
+EVEN = [  # prefixes whose key tiles are cut into equal runs over all heads (on 152 SMs)
+    (2, 1, 320, 320, 64, 3, [3, 0], 200),           # runs shorter than three heads
+    (3, 2, 160, 160, 128, 2, [2, 1, 0], 200),
+    (33, 8, 80, 80, 64, 8, [8] * 33, 199),          # three row tiles: a pair and one alone
+    (33, 8, 8, 8, 128, 8, [i % 9 for i in range(33)], 12743),
+    (100, 8, 20, 20, 64, 8, [8] * 100, 5001),       # seven row tiles; more tiles a run than fp32 output folds at
+]
+
+
+@pytest.mark.parametrize("kind,out_dtype,shape",
+                         [("int8", torch.float32, s) for s in EVEN[:3] + EVEN[4:]] +
+                         [("bf16", torch.bfloat16, s) for s in EVEN[:4]])
+def test_shared_prefix_in_equal_runs(kind, out_dtype, shape):
+    *own, P = shape
+    x = make(kind, *own, seed=P)
+    Hkv, d = shape[3], shape[4]
+    g = torch.Generator("cuda").manual_seed(P)
+    kp, vp = (torch.randn(Hkv, P, d, device="cuda", generator=g).bfloat16() for _ in range(2))
+    kp *= torch.linspace(0.2, 2.0, P, device="cuda")[None, :, None].bfloat16()   # maxima that move along the prefix
+    run_and_check_prefix(x, kp, vp, out_dtype)
+    q, k, v, qpos, kw = x
+    two = [sd().cache_attend(q, k, v, qpos, out_dtype=out_dtype, k_prefix=kp, v_prefix=vp, **kw) for _ in range(2)]
+    assert torch.equal(two[0][0], two[1][0]) and torch.equal(two[0][1], two[1][1])
+
+
 def run_and_check_prefix(x, kp, vp, out_dtype):
     # the prefix's weights are bf16 whatever the cache holds: held to the bf16 bound
     q, k, v, qpos, kw = x

@@ -66,7 +66,8 @@ struct CaParams {
     float* lse;
     int32_t* err;
     CaWorkspace ws;
-    int B, V, Hq, Hkv, G, R, T, n_idx, block, n_list, P, pre_splits, out_bf16;
+    PrefixPlan pre;
+    int B, V, Hq, Hkv, G, R, T, n_idx, block, n_list, P, out_bf16;
     float scale_log2;
 };
 
@@ -404,17 +405,6 @@ SD_DEVINL int seq_len(const CaParams& p, int b) {
 }
 SD_DEVINL unsigned tiles_of(int rows) { return (unsigned)max(1, (rows + kCaTile - 1) / kCaTile); }
 
-// W units cut into n runs (n <= W): the first W % n have one more.  The run that holds unit x.
-struct Cut {
-    unsigned q, rem;
-    SD_DEVINL Cut(unsigned W, unsigned n) : q(W / n), rem(W % n) {}
-    SD_DEVINL unsigned start(unsigned c) const { return c * q + min(c, rem); }
-    SD_DEVINL unsigned run_of(unsigned x) const {
-        const unsigned big = rem * (q + 1);
-        return x < big ? x / (q + 1) : rem + (x - big) / q;
-    }
-};
-
 SD_DEVINL void store_pair(void* out, bool bf16, size_t i, float x, float y) {  // elements i, i + 1 (i even)
     if (bf16)
         reinterpret_cast<uint32_t*>(out)[i / 2] = pack_bf16x2(x, y);
@@ -423,7 +413,7 @@ SD_DEVINL void store_pair(void* out, bool bf16, size_t i, float x, float y) {  /
 }
 
 // The sum of a query row's states start, start + step, ..: those of its group's runs (slots first ..
-// first + runs - 1) and of the prefix's splits.  Lane l holds columns kE l ..
+// first + runs - 1) and of the prefix's runs.  Lane l holds columns kE l ..
 template <int D>
 struct RowSum {
     static constexpr int kE = D / 32;
@@ -433,15 +423,16 @@ template <int D>
 SD_DEVINL RowSum<D> sum_states(const CaParams& p, int b, int kvh, int r, int first, int runs, int start, int step,
                                int lane) {
     constexpr int kE = RowSum<D>::kE;
-    const int n = runs + p.pre_splits;
+    const int2 pre = p.P > 0 ? p.pre.range(kvh) : make_int2(0, 0);
+    const int n = runs + pre.y;
     const unsigned M = (unsigned)p.B * p.R, mrow = (unsigned)b * p.R + r;
     auto ml_of = [&](int i) {
         return __ldcg(i < runs ? &p.ws.ml[(size_t)(first + i) * p.R + r]
-                               : &p.ws.pre_ml[((size_t)kvh * p.pre_splits + (i - runs)) * M + mrow]);
+                               : &p.ws.pre_ml[(size_t)(pre.x + i - runs) * M + mrow]);
     };
     auto o_of = [&](int i) {
         return i < runs ? p.ws.o + ((size_t)(first + i) * p.R + r) * D
-                        : p.ws.pre_o + (((size_t)kvh * p.pre_splits + (i - runs)) * M + mrow) * D;
+                        : p.ws.pre_o + ((size_t)(pre.x + i - runs) * M + mrow) * D;
     };
     RowSum<D> s;
     s.L = 0.f;
@@ -553,7 +544,7 @@ __global__ void __launch_bounds__(kCaThreads, MINB) cache_attend_kernel(const Ca
         if (p.P > 0) pdl_wait();  // (the merge kernel counts on the prefix being done)
         return;
     }
-    const Cut cut(W, ncta);
+    const Cut cut = Cut::of(W, ncta);
     w0 = cut.start(c);
     const unsigned w1 = cut.start(c + 1);
     if constexpr (SEL) {
@@ -957,7 +948,7 @@ CaPlan ca_plan(const sd_cache_attend_args* a) {
     const long units = NG * std::max<long>(1, (rows + kCaTile - 1) / kCaTile);
     pl.ctas = (int)std::min<long>(units, (long)num_sms() * ca_ctas_per_sm(ca_kind(a), a->d, R <= 8 ? 1 : 2, R <= 16 ? 1 : 2));
     pl.slots = (int)(pl.ctas + NG - 1);
-    pl.pre_splits = a->P > 0 ? prefix_splits(a) : 0;
+    if (a->P > 0) pl.pre = prefix_plan(a);
     return pl;
 }
 
@@ -1068,12 +1059,12 @@ extern "C" sd_status sd_cache_attend(const sd_cache_attend_args* a, void* stream
     p.block = a->block;
     p.n_list = a->idx != nullptr ? a->n_idx * a->block : 0;
     p.P = a->P;
-    p.pre_splits = pl.pre_splits;
+    p.pre = pl.pre;
     p.out_bf16 = a->out_dtype == SD_BF16;
     p.scale_log2 = a->scale * 1.44269504088896340736f;
     cudaStream_t cs = as_stream(stream);
     if (a->P > 0) {
-        st = prefix_launch(a, pl.pre_splits, w, cs);
+        st = prefix_launch(a, pl.pre, w, cs);
         if (st != SD_OK) return st;
     }
     const bool d128 = a->d == 128;

@@ -27,29 +27,39 @@ SD_DEVINL bool elect_one() {
     return p != 0u;
 }
 
-// Shared-memory matrix descriptor of an MN-major operand in the 128-byte swizzle layout: rows
-// of the K dimension, each 64 neighbouring elements (128 bytes) of the M or N dimension; 8-row groups
-// 1024 bytes apart (stride byte offset), the next 64 elements `chunk_bytes` further (leading
-// byte offset).
-SD_DEVINL uint64_t umma_desc_mn_sw128(uint32_t smem_byte_addr, uint32_t chunk_bytes) {
-    uint64_t d = 0;
-    d |= (uint64_t)((smem_byte_addr & 0x3FFFFu) >> 4);
-    d |= (uint64_t)(chunk_bytes >> 4) << 16;
-    d |= (uint64_t)(1024u >> 4) << 32;
-    d |= (uint64_t)1u << 46;
-    d |= (uint64_t)2u << 61;
-    return d;
+// Shared-memory matrix descriptors of the 128-byte swizzle layout: the low word has the address >> 4 (it can be
+// added to) and at bit 16 the leading byte offset >> 4, the high word is one constant (8-row groups 1024
+// bytes apart, version 1, swizzle mode 2; sums of 64-bit descriptors came out with a wrong high word where
+// the compiler was short of registers).  K-major: rows of 64 elements of the K dimension.  MN-major:
+// rows of the K dimension, each 64 neighbouring elements (128 bytes) of the M or N dimension, the next
+// 64 elements `chunk_bytes` further.
+constexpr uint32_t kUmmaSw128 = (1024u >> 4) | (1u << 14) | (2u << 29);
+SD_DEVINL uint32_t umma_lo_k(uint32_t smem_byte_addr) { return ((smem_byte_addr & 0x3FFFFu) >> 4) | (1u << 16); }
+SD_DEVINL uint32_t umma_lo_mn(uint32_t smem_byte_addr, uint32_t chunk_bytes) {
+    return ((smem_byte_addr & 0x3FFFFu) >> 4) | ((chunk_bytes >> 4) << 16);
 }
 // The instruction descriptor bit of an MN-major B operand.
 constexpr uint32_t kUmmaBMnMajor = 1u << 16;
 
-// D[tmem] (+)= A[tmem] * B[smem], A's 16-bit elements packed in pairs along K, one 32-bit column each.
-SD_DEVINL void umma_bf16_ta(uint32_t tmem_d, uint32_t tmem_a, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+// D[tmem] (+)= A[smem] * B[smem], descriptors by their low words.
+SD_DEVINL void umma_bf16_ss(uint32_t tmem_d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(tmem_d),
-        "r"(tmem_a), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        "mov.b64 a, {%1, %5};\n\t"
+        "mov.b64 b, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(tmem_d),
+        "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(kUmmaSw128)
+        : "memory");
+}
+// The same with A in TMEM, its 16-bit elements packed in pairs along K, one 32-bit column each.
+SD_DEVINL void umma_bf16_ts(uint32_t tmem_d, uint32_t tmem_a, uint32_t b_lo, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "mov.b64 b, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(tmem_d),
+        "r"(tmem_a), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(kUmmaSw128)
         : "memory");
 }
 
