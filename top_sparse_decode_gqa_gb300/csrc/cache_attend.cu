@@ -440,34 +440,40 @@ SD_DEVINL RowSum<D> sum_states(const CaParams& p, int b, int kvh, int r, int fir
 #pragma unroll
     for (int e = 0; e < kE; ++e) s.acc[e] = 0.f;
     for (int base = start; base < n; base += 32 * step) {
-        const int mine = base + step * lane;
+        const int mine = base + step * lane, cnt = min(32, (n - base + step - 1) / step);
         const float2 ml = mine < n ? ml_of(mine) : make_float2(kNone, 0.f);
+        // eight states' rows are loaded together, and the next eight before these are added
+        float x[2][8][kE];
+        auto load = [&](int k0, float (&to)[8][kE]) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const float* o = o_of(base + step * min(k0 + k, cnt - 1)) + kE * lane;
+                if constexpr (kE == 4) {
+                    const float4 y = __ldcg(reinterpret_cast<const float4*>(o));
+                    to[k][0] = y.x, to[k][1] = y.y, to[k][2] = y.z, to[k][3] = y.w;
+                } else {
+                    const float2 y = __ldcg(reinterpret_cast<const float2*>(o));
+                    to[k][0] = y.x, to[k][1] = y.y;
+                }
+            }
+        };
+        load(0, x[0]);
         const float was = s.top;
         s.top = fmaxf(was, warp_max(ml.x));
         const float f = exp2f(fmaxf(ml.x, kNone) - s.top), fo = exp2f(was - s.top);
         s.L = s.L * fo + ml.y * f;
 #pragma unroll
         for (int e = 0; e < kE; ++e) s.acc[e] *= fo;
-        const int cnt = min(32, (n - base + step - 1) / step);
-        for (int k0 = 0; k0 < cnt; k0 += 8) {  // eight states' rows loaded together
-            float x[8][kE];
+#pragma unroll
+        for (int k0 = 0; k0 < 32; k0 += 8) {
+            if (k0 >= cnt) break;
+            if (k0 + 8 < cnt) load(k0 + 8, x[(k0 / 8 + 1) & 1]);
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-                const float* o = o_of(base + step * min(k0 + k, cnt - 1)) + kE * lane;
-                if constexpr (kE == 4) {
-                    const float4 y = __ldcg(reinterpret_cast<const float4*>(o));
-                    x[k][0] = y.x, x[k][1] = y.y, x[k][2] = y.z, x[k][3] = y.w;
-                } else {
-                    const float2 y = __ldcg(reinterpret_cast<const float2*>(o));
-                    x[k][0] = y.x, x[k][1] = y.y;
-                }
-            }
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const float fk = __shfl_sync(0xffffffffu, f, min(k0 + k, 31));
+                const float fk = __shfl_sync(0xffffffffu, f, k0 + k);
                 if (k0 + k < cnt) {
 #pragma unroll
-                    for (int e = 0; e < kE; ++e) s.acc[e] = fmaf(x[k][e], fk, s.acc[e]);
+                    for (int e = 0; e < kE; ++e) s.acc[e] = fmaf(x[(k0 / 8) & 1][k][e], fk, s.acc[e]);
                 }
             }
         }
