@@ -141,3 +141,10 @@ def test_an_empty_cache_for_the_host_side(sd):
     k, v, ks, vs = sd.q8_cache(2, 3, 5, 64, torch.float8_e4m3fn, device="cpu")
     assert k.shape == v.shape == (2, 3, 5, 64) and k.dtype == torch.float8_e4m3fn
     assert ks.shape == vs.shape == (2, 3, 5) and not bool(ks.any())
+
+
+def test_a_workspace_of_the_host_is_refused(sd):
+    a = sd.sd_cache_attend_args()
+    with pytest.raises(ValueError, match="workspace must be a contiguous CUDA tensor"):
+        sd.prepare_cache_attend(a, workspace=torch.empty(4096, dtype=torch.uint8))
+    assert not a.workspace and a.workspace_bytes == 0

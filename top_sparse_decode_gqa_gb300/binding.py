@@ -774,6 +774,11 @@ def sd_cache_attend(args: sd_cache_attend_args, stream=None) -> None:
     _check(lib().sd_cache_attend(ctypes.byref(args), _stream(stream)), "sd_cache_attend")
 
 
+def _use_workspace(args: sd_cache_attend_args, workspace: torch.Tensor):
+    _same_device(workspace=(workspace, workspace.dtype, workspace.shape))
+    args.workspace, args.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
 def cache_attend(q, k_cache, v_cache, qpos, workspace=None, stream=None, **kw):
     """Convenience wrapper: builds the args, makes a workspace if none is given (see
     cache_attend_workspace), runs the call and returns (out, lse)."""
@@ -784,7 +789,7 @@ def cache_attend(q, k_cache, v_cache, qpos, workspace=None, stream=None, **kw):
             stream = torch.cuda.ExternalStream(_stream(stream).value or 0)
         with torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext():
             workspace = cache_attend_workspace(a)
-    a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    _use_workspace(a, workspace)
     sd_cache_attend(a, stream)
     return out, lse
 
@@ -878,7 +883,7 @@ def prepare_q8_append(k_new, v_new, k_codes, v_codes, k_scale, v_scale, pos0, co
 
 def prepare_cache_attend(args: sd_cache_attend_args, workspace=None, stream=None) -> PreparedCall:
     if workspace is not None:
-        args.workspace, args.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+        _use_workspace(args, workspace)
     return PreparedCall("sd_cache_attend", ctypes.byref(args), _stream(stream))
 
 
