@@ -47,6 +47,7 @@
 #include <cmath>
 
 #include "cache_attend.cuh"
+#include "tc_operands.cuh"
 
 namespace sd {
 namespace {
@@ -163,6 +164,7 @@ SD_DEVINL int perm(int i) {
 // ------------------------------------------------------------------ a warp's state
 
 constexpr float kNone = -1e30f;    // a maximum over no rows (finite: differences of it stay numbers)
+constexpr int kNoPos = 0x7fffffff; // the position of a row that is none
 constexpr float kGrow = 4.f;       // how far (base 2) a weight may pass its maximum before that moves
 constexpr float kTopF16 = 10.f;    // log2 of the largest product weight when its maximum has just moved
 constexpr float kLimF16 = 32768.f; // the product weight at which it moves
@@ -258,40 +260,43 @@ SD_DEVINL void ca_scores(const uint8_t* st, const Queries<D, NQ>& q, int lane, f
 }
 
 // The online softmax of a step: s becomes the weights of the V rows.  Unless every query sees all
-// rows of the step (all), those above a query's limit (sl[8nq + 2t4 + e]) take no part (pos: the
-// positions of rows perm(g8), perm(g8) + 8).
-template <int KIND, int D, int NQ>
-SD_DEVINL void ca_softmax(float (&s)[NQ][4], const float (&ks)[2], const float (&vs)[2], const int (&pos)[2], bool all,
+// rows of the step (all), those above a query's limit (sl[8nq + 2t4 + e]) take no part (pos(h): the
+// position of row perm(g8) + 8h).
+template <int KIND, int D, int NQ, class Pos>
+SD_DEVINL void ca_softmax(float (&s)[NQ][4], const float (&ks)[2], const float (&vs)[2], Pos pos, bool all,
                           const int* sl, int t4, const Queries<D, NQ>& q, CaState<D, NQ>& st) {
     constexpr bool F16 = KIND != kBf16;
     float top = -INFINITY, wide = 0.f;
-    float w[NQ][4];
+    float w[NQ][4], z[NQ][4];  // weights, and what makes a logit of s
     auto weights = [&]() {
 #pragma unroll
         for (int nq = 0; nq < NQ; ++nq)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int e = i & 1, h = i >> 1;
-                const float dx = s[nq][i] - st.m[nq][e];
-                top = fmaxf(top, dx);
-                const float p = fast_exp2(dx);
-                w[nq][i] = p;
-                if constexpr (F16) wide = fmaxf(wide, p * vs[h] * st.c[nq][e]);
+            for (int e = 0; e < 2; ++e) {
+                float dx[2], pw[2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    dx[h] = fmaf(s[nq][2 * h + e], z[nq][2 * h + e], -st.m[nq][e]);
+                    w[nq][2 * h + e] = fast_exp2(dx[h]);
+                    if constexpr (F16) pw[h] = w[nq][2 * h + e] * vs[h] * st.c[nq][e];
+                }
+                top = max3(top, dx[0], dx[1]);
+                if constexpr (F16) wide = max3(wide, pw[0], pw[1]);
             }
     };
 #pragma unroll
     for (int nq = 0; nq < NQ; ++nq)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int e = i & 1, h = i >> 1;
-            s[nq][i] *= F16 ? ks[h] * q.qs[nq][e] : q.qs[nq][e];
-        }
+        for (int i = 0; i < 4; ++i) z[nq][i] = F16 ? ks[i >> 1] * q.qs[nq][i & 1] : q.qs[nq][i & 1];
     if (!all) {
+        const int at[2] = {pos(0), pos(1)};
 #pragma unroll
         for (int nq = 0; nq < NQ; ++nq)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (pos[i >> 1] > sl[8 * nq + 2 * t4 + (i & 1)]) s[nq][i] = -INFINITY;
+            for (int i = 0; i < 4; ++i) {
+                s[nq][i] = at[i >> 1] > sl[8 * nq + 2 * t4 + (i & 1)] ? -INFINITY : s[nq][i] * z[nq][i];
+                z[nq][i] = 1.f;
+            }
     }
     weights();
     if (__any_sync(0xffffffffu, top > kGrow || wide > kLimF16)) {
@@ -299,14 +304,15 @@ SD_DEVINL void ca_softmax(float (&s)[NQ][4], const float (&ks)[2], const float (
         for (int nq = 0; nq < NQ; ++nq)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
+                const float x0 = s[nq][e] * z[nq][e], x1 = s[nq][2 + e] * z[nq][2 + e];
                 const float mo = st.m[nq][e];
-                const float mn = fmaxf(mo, max_over_rows(fmaxf(s[nq][e], s[nq][2 + e])));
+                const float mn = fmaxf(mo, max_over_rows(fmaxf(x0, x1)));
                 const float fl = fast_exp2(mo - mn);
                 float fo = fl;
                 if constexpr (F16) {
                     // log2 of a zero scale is -inf: its row asks for nothing.  The product's maximum is never so
                     // far below m that c would overflow
-                    float y = fmaxf(s[nq][e] + __log2f(vs[0]), s[nq][2 + e] + __log2f(vs[1]));
+                    float y = fmaxf(x0 + __log2f(vs[0]), x1 + __log2f(vs[1]));
                     y = max_over_rows(y);
                     const float co = st.c[nq][e];
                     const float m2o = co > 0.f ? mo + kTopF16 - __log2f(co) : kNone;
@@ -648,13 +654,19 @@ __global__ void __launch_bounds__(kCaThreads, MINB) cache_attend_kernel(const Ca
         // Copies the team's rows of a step (resolved in `rows`) into a stage of its ring, a row that is none
         // as zeros (whatever the cache holds there, its weight of 0 must not meet a NaN or an infinity).
         // A team of two shares the copies: K, V.
-        auto fetch = [&](int stage, int rows) {
+        auto fetch = [&](int stage, int step, int rows) {
             uint8_t* st = sh.ring[team][stage];
             constexpr int kPer = 32 / S::kChunks > 0 ? 32 / S::kChunks : 1;  // rows an instruction copies
             const int c0 = lane % S::kChunks, r0 = lane / S::kChunks;
 #pragma unroll
             for (int r = 0; r < 16; r += kPer) {
-                const int t = __shfl_sync(0xffffffffu, rows, r + r0);
+                int t;
+                if constexpr (SEL) {
+                    t = __shfl_sync(0xffffffffu, rows, r + r0);
+                } else {
+                    t = j0 + 16 * step + r + r0;
+                    if (t >= j1) t = -1;
+                }
                 const size_t off = (size_t)max(t, 0) * kRow + 16 * c0;
                 const uint32_t n = t < 0 ? 0u : 16u;
                 const int to = S::at(r + r0, c0);
@@ -664,7 +676,7 @@ __global__ void __launch_bounds__(kCaThreads, MINB) cache_attend_kernel(const Ca
             if (half == 0) {
                 if constexpr (F16)
                     cp_async4_zfill(st + S::oKs + 4 * lane, (lane < 16 ? ksb : vsb) + max(rows, 0), rows < 0 ? 0u : 4u);
-                if (lane < 16) reinterpret_cast<int*>(st + S::oPos)[lane] = rows < 0 ? 0x7fffffff : rows;
+                if (SEL && lane < 16) reinterpret_cast<int*>(st + S::oPos)[lane] = rows < 0 ? kNoPos : rows;
             }
         };
         auto team_sync = [&]() {
@@ -679,7 +691,7 @@ __global__ void __launch_bounds__(kCaThreads, MINB) cache_attend_kernel(const Ca
         for (int i = 0; i < kStages; ++i) early[i] = resolve(team + i * kTeams);
 #pragma unroll
         for (int i = 0; i + 1 < kStages; ++i) {
-            if (team + i * kTeams < nsteps) fetch(i, early[i]);
+            if (team + i * kTeams < nsteps) fetch(i, team + i * kTeams, early[i]);
             cp_async_commit();
         }
         int rows = early[kStages - 1];
@@ -806,21 +818,24 @@ __global__ void __launch_bounds__(kCaThreads, MINB) cache_attend_kernel(const Ca
                 // which takes the rows kStages - 1 steps ahead
                 cp_async_wait<kStages - 2>();
                 team_sync();
-                if (n + (kStages - 1) * kTeams < nsteps) fetch(stage == 0 ? kStages - 1 : stage - 1, rows);
+                if (n + (kStages - 1) * kTeams < nsteps) fetch(stage == 0 ? kStages - 1 : stage - 1, n + (kStages - 1) * kTeams, rows);
                 cp_async_commit();
                 rows = resolve(n + kStages * kTeams);
                 const uint8_t* at = sh.ring[team][stage];
                 const int row = perm(g8);
                 float sc[NQ][4], ks[2], vs[2];
-                int pos[2];
                 ca_scores<KIND, D, NQ>(at, q, lane, sc);
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    pos[h] = reinterpret_cast<const int*>(at + S::oPos)[row + 8 * h];
                     ks[h] = reinterpret_cast<const float*>(at + S::oKs)[row + 8 * h];
                     vs[h] = reinterpret_cast<const float*>(at + S::oVs)[row + 8 * h];
                 }
-                const bool all = SEL ? __all_sync(0xffffffffu, max(pos[0], pos[1]) < lmin) : j0 + 16 * n + 16 <= lmin;
+                auto pos = [&](int h) {
+                    if constexpr (SEL) return reinterpret_cast<const int*>(at + S::oPos)[row + 8 * h];
+                    const int i = j0 + 16 * n + row + 8 * h;
+                    return i < j1 ? i : kNoPos;
+                };
+                const bool all = SEL ? __all_sync(0xffffffffu, max(pos(0), pos(1)) < lmin) : j0 + 16 * n + 16 <= lmin;
                 ca_softmax<KIND, D, NQ>(sc, ks, vs, pos, all, lim, t4, q, st);
                 ca_output<KIND, D, NQ, HILO>(at, lane, sc, st);
                 stage = stage == kStages - 1 ? 0 : stage + 1;
