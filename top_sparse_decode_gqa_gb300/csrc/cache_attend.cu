@@ -21,7 +21,7 @@
 // what they stand for, which one vote a step finds out; until then no value crosses lanes.
 // The tensor cores cut what they add to a sum (2^-24 of it), so SD_F32 output folds the
 // accumulators into fp32 sums in shared memory every 32 steps (a 131072-row cache: 1.5e-5 of
-// error in the output without, 3e-6 with).
+// error in the output without, 1e-6 with).
 //
 // Bound: HBM; for more than 16 query rows the tensor cores' mma.sync rate comes close (8 cycles an
 // instruction: 174 us against 163 us of loads for 4 x 131072 int8 rows and 32 query rows in two-part
