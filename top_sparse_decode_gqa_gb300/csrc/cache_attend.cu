@@ -25,7 +25,8 @@
 //
 // Bound: HBM; for more than 16 query rows the tensor cores' mma.sync rate comes close (8 cycles an
 // instruction: 174 us against 163 us of loads for 4 x 131072 int8 rows and 32 query rows in two-part
-// weights).  A warp takes 8 or 16 query rows; for 17 to 32 two warps make a team that shares the
+// weights; the kernel takes 421, waiting for instructions: about 500 a warp and step, 12 warps an SM).  8 ragged
+// e4m3 caches of 346 MB: 59 us, 5.9 TB/s.  A warp takes 8 or 16 query rows; for 17 to 32 two warps make a team that shares the
 // fetched rows.  A team copies its steps of 16 K and V rows into a ring of 2 or 3 stages of its own
 // (cp.async), so loads of the next steps are in flight through this one's arithmetic and no barrier is
 // wider than a team.  The contraction over d may run in any order, so a lane takes 16 neighbouring
